@@ -1,10 +1,11 @@
 """Python binding of libiqcodec.so: MI355X-native importance-weighted IQ1_S /
 IQ2_XS codebook-search encode, decode, candidate emission and local-Hessian
-choice search.
+choice search; and the layer operators of ``layers.py``: products in 8-bit
+integers, dense and by expert, and the routing of tokens to experts.
 
 This module only marshals arguments: it checks tensors, takes their device
 pointers and the current HIP stream from PyTorch, and calls the C-ABI declared
-in ``include/iq_codec.h``.  Every step of the computation runs in the HIP
+in ``include/iq_codec.h`` and ``include/iq_layers.h``.  Every step of the computation runs in the HIP
 kernels of the library.  There is no CPU path: if the library is not built, or
 the device is not a gfx950 GPU, calls raise.
 """
@@ -15,6 +16,8 @@ import ctypes
 import os
 
 import torch  # noqa: F401  (device memory and streams; loads the HIP runtime first)
+
+from . import layers as _layers
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libiqcodec.so")
@@ -27,7 +30,7 @@ NUM_CHOICES = {"iq1_s": 16, "iq2_xs": 16, "iq1_m": 8}
 STATUS = {
     0: "IQ_OK", 1: "IQ_ERR_NULL", 2: "IQ_ERR_FORMAT", 3: "IQ_ERR_SHAPE", 4: "IQ_ERR_GRID",
     5: "IQ_ERR_NONFINITE", 6: "IQ_ERR_IMPORTANCE", 7: "IQ_ERR_SCALE_RANGE", 8: "IQ_ERR_ARG",
-    9: "IQ_ERR_CODE", 10: "IQ_ERR_HIP", 11: "IQ_ERR_DEVICE",
+    9: "IQ_ERR_CODE", 10: "IQ_ERR_HIP", 11: "IQ_ERR_DEVICE", 12: "IQ_ERR_INDEX",
 }
 
 
@@ -81,6 +84,7 @@ def load(build_if_missing: bool = True):
     L.iq_choice_search.restype = ctypes.c_int
     L.iq_choice_search_blocks.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P]
     L.iq_choice_search_blocks.restype = ctypes.c_int
+    _layers.declare(L)
     _lib = L
     return L
 
@@ -364,3 +368,8 @@ def choice_search(H, cand_err, *, sweeps=2, trace=False):
                                           _ptr(picks), _ptr(tr), _stream())
     _check(code, "iq_choice_search_blocks")
     return (picks, tr) if trace else picks
+
+
+from .layers import (  # noqa: E402  (they use the helpers above)
+    expert_combine, expert_combine_backward, expert_dispatch, expert_dispatch_backward,
+    expert_sort, int8_expert_matmul, int8_linear, int8_matmul, quantize_rows)

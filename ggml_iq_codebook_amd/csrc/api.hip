@@ -10,8 +10,14 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_common.hpp"
 #include "iq_codec.h"
 #include "launch.hpp"
+
+using iqk::aligned;
+using iqk::check_device;
+using iqk::from_hip;
+using iqk::run_with_status;
 
 namespace {
 
@@ -20,9 +26,9 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_kind[kMaxDevices];
 std::atomic<int> g_device_cus[kMaxDevices];
 
-// Also records the device's compute units in g (when given): persistent
-// launches size their grid by it.
-iq_status_t check_device(iqk::BlockGeom* g = nullptr)
+}  // namespace
+
+iq_status_t iqk::check_device(int* cus)
 {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return IQ_ERR_HIP;
@@ -36,11 +42,11 @@ iq_status_t check_device(iqk::BlockGeom* g = nullptr)
                                 std::memory_order_relaxed);
         g_device_kind[dev].store(kind, std::memory_order_release);
     }
-    if (g) g->cus = g_device_cus[dev].load(std::memory_order_relaxed);
+    if (cus) *cus = g_device_cus[dev].load(std::memory_order_relaxed);
     return kind == 1 ? IQ_OK : IQ_ERR_DEVICE;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 // Geometry of [batch][rows][cols] with every size positive and cols % 256 == 0.
 iq_status_t geometry(int64_t batch, int64_t rows, int64_t cols, iqk::BlockGeom* g)
@@ -58,8 +64,6 @@ iq_status_t geometry(int64_t batch, int64_t rows, int64_t cols, iqk::BlockGeom* 
     if (g->nblocks > (INT64_C(1) << 34)) return IQ_ERR_SHAPE;
     return IQ_OK;
 }
-
-iq_status_t from_hip(hipError_t e) { return e == hipSuccess ? IQ_OK : IQ_ERR_HIP; }
 
 // ---------------------------------------------------------------------------
 // Calls made with status = NULL synchronize their stream and return the first
@@ -79,13 +83,12 @@ __global__ void clear_sync_word_kernel(int32_t* word) { word[0] = 0; }
 std::mutex g_sync_mutex[kMaxDevices];
 int32_t* g_sync_word[kMaxDevices];    // guarded by g_sync_mutex[dev]
 
-// Runs launch(status) when the caller gave a status word.  Otherwise clears
-// the device's own word, runs launch(word), waits for the stream and returns
-// the word: IQ_OK, or the first data error code the kernels reported.
-template <class Launch>
-iq_status_t run_with_status(int32_t* status, hipStream_t stream, Launch&& launch)
+}  // namespace
+
+// Clears the device's own word, runs launch(word), waits for the stream and
+// returns the word: IQ_OK, or the first data error code the kernels reported.
+iq_status_t iqk::run_synced(hipStream_t stream, hipError_t (*launch)(void*, int32_t*), void* what)
 {
-    if (status) return from_hip(launch(status));
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return IQ_ERR_HIP;
     if (dev < 0 || dev >= kMaxDevices) return IQ_ERR_DEVICE;
@@ -99,13 +102,15 @@ iq_status_t run_with_status(int32_t* status, hipStream_t stream, Launch&& launch
     int32_t* word = g_sync_word[dev];
     hipLaunchKernelGGL(clear_sync_word_kernel, dim3(1), dim3(1), 0, stream, word);
     if (hipGetLastError() != hipSuccess) return IQ_ERR_HIP;
-    if (launch(word) != hipSuccess) return IQ_ERR_HIP;
+    if (launch(what, word) != hipSuccess) return IQ_ERR_HIP;
     int32_t host = 0;
     if (hipMemcpyAsync(&host, word, sizeof(host), hipMemcpyDeviceToHost, stream) != hipSuccess ||
         hipStreamSynchronize(stream) != hipSuccess)
         return IQ_ERR_HIP;
     return static_cast<iq_status_t>(host);
 }
+
+namespace {
 
 bool known_format(iq_format_t fmt)
 {
@@ -175,6 +180,7 @@ const char* iq_status_str(iq_status_t st)
     case IQ_ERR_CODE: return "payload grid index beyond the grid";
     case IQ_ERR_HIP: return "HIP runtime error";
     case IQ_ERR_DEVICE: return "current device is not gfx950";
+    case IQ_ERR_INDEX: return "expert index out of range";
     }
     return "unknown status";
 }
@@ -195,7 +201,7 @@ iq_status_t iq_encode(iq_format_t fmt, iq_dtype_t wdtype, const void* w, int64_t
         !aligned(out, 2) || (scales && !aligned(scales, 2)) || (choices && !aligned(choices, 4)) ||
         (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
-    st = check_device(&g);
+    st = check_device(&g.cus);
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
         return launch_encode(fmt, wdtype, w, importance, grid, grid_size, scales, choices, out,
@@ -219,7 +225,7 @@ iq_status_t iq_encode_every_choice(iq_format_t fmt, iq_dtype_t wdtype, const voi
     if (!aligned(w, 16) || !aligned(grid, 16) || (importance && !aligned(importance, 16)) ||
         !aligned(out, 2) || (scales && !aligned(scales, 2)) || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
-    st = check_device(&g);
+    st = check_device(&g.cus);
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
         return launch_encode(fmt, wdtype, w, importance, grid, grid_size, scales, nullptr, out,
@@ -249,7 +255,7 @@ iq_status_t iq_fake_quant(iq_format_t fmt, iq_dtype_t wdtype, const void* w, int
     const uintptr_t wbytes = static_cast<uintptr_t>(g.nblocks) * 256u * dtype_bytes(wdtype);
     const uintptr_t xbytes = static_cast<uintptr_t>(g.nblocks) * 256u * sizeof(float);
     if (x0 < w0 + wbytes && w0 < x0 + xbytes) return IQ_ERR_ARG;
-    st = check_device(&g);
+    st = check_device(&g.cus);
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
         return launch_encode(fmt, wdtype, w, importance, grid, grid_size, scales, choices, out,
@@ -269,7 +275,7 @@ iq_status_t iq_dequant(iq_format_t fmt, const uint8_t* packed, int64_t batch, in
     if (grid_size < 1 || grid_size > grid_max(fmt)) return IQ_ERR_GRID;
     if (!aligned(grid, 16) || !aligned(out, 16) || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
-    st = check_device(&g);
+    st = check_device(&g.cus);
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
         return iqk::launch_dequant((int)fmt, packed, grid, grid_size, out, s, g, stream);
@@ -294,7 +300,7 @@ iq_status_t iq_encode_candidates(iq_format_t fmt, iq_dtype_t wdtype, const void*
         !aligned(cand_err, 16) || !aligned(cand_choice, 4) ||
         (cand_codes && !aligned(cand_codes, 2)) || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
-    st = check_device(&g);
+    st = check_device(&g.cus);
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
         if (fmt != IQ_FMT_IQ2_XS)

@@ -1,0 +1,446 @@
+// expert_route.hip -- tokens sorted by expert, copied there and brought back
+// with the router's weights, and the gradients of both copies.
+//
+// The sort is a stable counting sort: counts per expert and chunk of choices,
+// their sums, then each choice's rank among the equal ones before it.  Nothing
+// depends on the order of atomics: they only add counts.  Dropped choices (-1)
+// count as one more expert behind the last, so `position` is a permutation of
+// all choices and every row of a sorted tensor has exactly one writer.
+//
+// The copies are bound by HBM.  They go token by token: a token's row is read
+// once for all its choices (dispatch), or its choices' rows are read and
+// summed in registers (combine), 16 bytes a lane, with no intermediate tensor
+// and no atomics.
+#include <hip/hip_runtime.h>
+
+#include "iq_layers.h"
+#include "layers_common.hpp"
+#include "layers_launch.hpp"
+
+namespace iqk {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The sort
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kMaxKeys = IQ_MAX_EXPERTS + 1;
+static_assert(kMaxKeys <= kSortThreads, "a thread per key");
+constexpr int64_t kChunkChoices = 4096;
+constexpr int kMaxChunks = 256;
+
+// The choice at place i as a key 0..experts, experts where it is dropped.
+template <class Choice>
+__device__ __forceinline__ int key_of(const Choice* choice, int64_t i, int experts, bool* bad)
+{
+    const Choice c = choice[i];
+    if (c >= 0 && c < (Choice)experts) return (int)c;
+    *bad = *bad || c != (Choice)-1;
+    return experts;
+}
+
+// Counts of a chunk's keys.
+template <class Choice>
+__global__ __launch_bounds__(kSortThreads) void expert_count_kernel(
+    const Choice* __restrict__ choice, int64_t n, int64_t per_chunk, int experts,
+    int32_t* __restrict__ counts)
+{
+    __shared__ int32_t count[kMaxKeys];
+    for (int e = threadIdx.x; e <= experts; e += kSortThreads) count[e] = 0;
+    __syncthreads();
+    const int64_t first = blockIdx.x * per_chunk;
+    const int64_t last = min(first + per_chunk, n);
+    bool bad = false;
+    for (int64_t i = first + threadIdx.x; i < last; i += kSortThreads)
+        atomicAdd(&count[key_of(choice, i, experts, &bad)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= experts; e += kSortThreads)
+        counts[(int64_t)blockIdx.x * (experts + 1) + e] = count[e];
+}
+
+// Places a chunk's choices.  Each wave takes a consecutive part of the chunk
+// and counts it in a row of its own, so the ranks follow the order of the
+// choices: chunk, wave, step of 64, lane.
+template <class Choice>
+__global__ __launch_bounds__(kSortThreads) void expert_place_kernel(
+    const Choice* __restrict__ choice, int64_t n, int64_t per_chunk, int experts,
+    const int32_t* __restrict__ counts, int32_t* __restrict__ order,
+    int32_t* __restrict__ position, int32_t* __restrict__ offsets, int32_t* status)
+{
+    extern __shared__ int32_t shared[];
+    const int keys = experts + 1;
+    int32_t* before = shared;                     // [waves][keys]: then the next place
+    int32_t* total = shared + kSortWaves * keys;  // [keys]: over all chunks
+    int32_t* start = total + keys;                // [keys]: of the chunks before this one
+    __shared__ int32_t wave_sums[kSortWaves];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t first = blockIdx.x * per_chunk;
+    const int64_t last = min(first + per_chunk, n);
+
+    for (int i = threadIdx.x; i < (kSortWaves + 2) * keys; i += kSortThreads) shared[i] = 0;
+    __syncthreads();
+
+    // This chunk's keys, counted per wave.
+    const int64_t per_wave = ((per_chunk + kSortThreads - 1) / kSortThreads) * kWave;
+    const int64_t wfirst = first + wave * per_wave;
+    const int64_t wlast = min(wfirst + per_wave, last);
+    bool bad = false;
+    for (int64_t i = wfirst + lane; i < wlast; i += kWave)
+        atomicAdd(&before[wave * keys + key_of(choice, i, experts, &bad)], 1);
+    if (bad) report_generic(status, IQ_ERR_INDEX);
+    // The other chunks' counts: several threads a key, each over some chunks.
+    if (gridDim.x > 1) {
+        const int groups = kSortThreads / keys;
+        const int group = threadIdx.x / keys, e = threadIdx.x % keys;
+        if (group < groups) {
+            int32_t all = 0, prior = 0;
+            for (int c = group; c < (int)gridDim.x; c += groups) {
+                const int32_t v = counts[(int64_t)c * keys + e];
+                all += v;
+                prior += c < (int)blockIdx.x ? v : 0;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&start[e], prior);
+        }
+    }
+    __syncthreads();
+    if (gridDim.x == 1) {
+        for (int e = threadIdx.x; e < keys; e += kSortThreads) {
+            int32_t all = 0;
+            for (int w = 0; w < kSortWaves; ++w) all += before[w * keys + e];
+            total[e] = all;
+        }
+        __syncthreads();
+    }
+    // First place of each key: the sum over the keys before it.
+    {
+        const int e = threadIdx.x;
+        const int32_t mine = e < keys ? total[e] : 0;
+        int32_t sum = mine;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int32_t up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        if (lane == kWave - 1) wave_sums[wave] = sum;
+        __syncthreads();
+        int32_t place = sum - mine;
+        for (int w = 0; w < wave; ++w) place += wave_sums[w];
+        if (e < keys) {
+            if (blockIdx.x == 0) offsets[e] = place;
+            // and of this chunk's waves
+            int32_t next = place + start[e];
+            for (int w = 0; w < kSortWaves; ++w) {
+                const int32_t c = before[w * keys + e];
+                before[w * keys + e] = next;
+                next += c;
+            }
+        }
+        __syncthreads();
+    }
+    // Ranks: lanes with the same key find each other bit by bit.
+    int bits = 0;
+    while ((1 << bits) < keys) ++bits;
+    const uint64_t below = (1ull << lane) - 1ull;
+    for (int64_t i0 = wfirst; i0 < wlast; i0 += kWave) {
+        const int64_t i = i0 + lane;
+        const bool live = i < wlast;
+        const int key = live ? key_of(choice, i, experts, &bad) : 0;
+        uint64_t same = __ballot(live);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((key >> b) & 1);
+            same &= ((key >> b) & 1) ? set : ~set;
+        }
+        int32_t* next = &before[wave * keys + key];
+        const int32_t base = live ? *next : 0;
+        const int32_t rank = __popcll(same & below);
+        // All lanes have read the row's counter before its first lane advances
+        // it: a wave's LDS accesses are done in order.
+        __builtin_amdgcn_wave_barrier();
+        if (live && rank == 0) *next = base + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (live) {
+            position[i] = base + rank;
+            order[base + rank] = (int32_t)i;
+        }
+    }
+}
+
+__global__ void no_choices_kernel(int32_t* offsets, int keys)
+{
+    for (int e = threadIdx.x; e < keys; e += blockDim.x) offsets[e] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// The copies
+// ---------------------------------------------------------------------------
+
+constexpr int kThreads = 256;
+
+// A row is shared by `lanes` threads (a power of two), 16 bytes a lane.  The
+// addresses need the alignment of a value only (global memory instructions
+// take any address; memcpy tells the compiler); the last vector of a row whose
+// width is no multiple goes value by value.
+template <int kDT>
+struct Row {
+    typedef typename Value<kDT>::raw raw;
+    static constexpr int kN = 16 / (int)sizeof(raw);
+    uint32_t u[4];
+    __device__ __forceinline__ raw get(int i) const
+    {
+        return sizeof(raw) == 4 ? (raw)u[i] : (raw)(u[i / 2] >> (16 * (i % 2)));
+    }
+    __device__ __forceinline__ void load(const raw* row, int64_t at, int64_t width)
+    {
+        if (at + kN <= width) {
+            __builtin_memcpy(u, row + at, 16);
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (at + i < width) put(i, row[at + i]);
+        }
+    }
+    __device__ __forceinline__ void store(raw* row, int64_t at, int64_t width) const
+    {
+        if (at + kN <= width) {
+            __builtin_memcpy(row + at, u, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (at + i < width) row[at + i] = get(i);
+        }
+    }
+    __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0u; }
+    // Value i of a vector that held 0 there.
+    __device__ __forceinline__ void put(int i, raw r)
+    {
+        if (sizeof(raw) == 4)
+            u[i] = r;
+        else
+            u[i / 2] |= (uint32_t)r << (16 * (i % 2));
+    }
+    __device__ __forceinline__ float operator[](int i) const { return Value<kDT>::load(get(i)); }
+    __device__ __forceinline__ void set(int i, float f) { put(i, Value<kDT>::store(f)); }
+};
+
+// The place of a token's choice: -1 outside the sorted rows (skipped).
+__device__ __forceinline__ int64_t place_of(const Route& r, int64_t token, int j)
+{
+    const int32_t p = r.position[token * r.top_k + j];
+    return p >= 0 && p < r.tokens * r.top_k ? p : -1;
+}
+
+template <int kDT>
+__global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
+                                                                   const void* __restrict__ x,
+                                                                   int64_t ldx,
+                                                                   void* __restrict__ sorted,
+                                                                   int64_t lds, int lanes)
+{
+    typedef typename Value<kDT>::raw raw;
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    if (token >= r.tokens) return;
+    const int64_t kept = *r.kept;
+    const raw* xr = static_cast<const raw*>(x) + token * ldx;
+    for (int64_t at = (int64_t)(threadIdx.x % lanes) * Row<kDT>::kN; at < r.width;
+         at += (int64_t)lanes * Row<kDT>::kN) {
+        Row<kDT> v, none;
+        v.load(xr, at, r.width);
+        none.zero();
+        for (int j = 0; j < r.top_k; ++j) {
+            const int64_t p = place_of(r, token, j);
+            if (p < 0) continue;
+            raw* to = static_cast<raw*>(sorted) + p * lds;
+            if (p < kept)
+                v.store(to, at, r.width);
+            else
+                none.store(to, at, r.width);
+        }
+    }
+}
+
+// kWeighted: combine; otherwise the gradient of dispatch.
+template <int kDT, bool kWeighted>
+__global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
+                                                                  const void* __restrict__ y,
+                                                                  int64_t ldy,
+                                                                  const float* __restrict__ weights,
+                                                                  void* __restrict__ out,
+                                                                  int64_t ldo, int lanes)
+{
+    typedef typename Value<kDT>::raw raw;
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    if (token >= r.tokens) return;
+    const int64_t kept = *r.kept;
+    raw* to = static_cast<raw*>(out) + token * ldo;
+    for (int64_t at = (int64_t)(threadIdx.x % lanes) * Row<kDT>::kN; at < r.width;
+         at += (int64_t)lanes * Row<kDT>::kN) {
+        float sum[Row<kDT>::kN] = {};
+        for (int j = 0; j < r.top_k; ++j) {
+            const int64_t p = place_of(r, token, j);
+            if (p < 0 || p >= kept) continue;
+            Row<kDT> v;
+            v.load(static_cast<const raw*>(y) + p * ldy, at, r.width);
+            const float w = kWeighted ? weights[token * r.top_k + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < Row<kDT>::kN; ++i) sum[i] += kWeighted ? w * v[i] : v[i];
+        }
+        Row<kDT> o;
+        o.zero();
+#pragma unroll
+        for (int i = 0; i < Row<kDT>::kN; ++i) o.set(i, sum[i]);
+        o.store(to, at, r.width);
+    }
+}
+
+// A workgroup per token: its gradient is scaled into the rows of its choices,
+// and multiplied with what those rows held, choice by choice.
+template <int kDT>
+__global__ __launch_bounds__(kThreads) void expert_combine_backward_kernel(
+    Route r, const void* __restrict__ out_grad, int64_t ldo, const void* __restrict__ y,
+    int64_t ldy, const float* __restrict__ weights, void* __restrict__ y_grad, int64_t ldg,
+    float* __restrict__ weights_grad)
+{
+    typedef typename Value<kDT>::raw raw;
+    __shared__ float parts[kThreads / kWave];
+    const int64_t token = blockIdx.x;
+    const int64_t kept = *r.kept;
+    const raw* gr = static_cast<const raw*>(out_grad) + token * ldo;
+    for (int j = 0; j < r.top_k; ++j) {
+        const int64_t p = place_of(r, token, j);
+        const bool live = p >= 0 && p < kept;
+        const float w = live ? weights[token * r.top_k + j] : 0.0f;
+        float dot = 0.0f;
+        if (p >= 0) {
+            const raw* yr = static_cast<const raw*>(y) + p * ldy;
+            raw* to = static_cast<raw*>(y_grad) + p * ldg;
+            for (int64_t at = (int64_t)threadIdx.x * Row<kDT>::kN; at < r.width;
+                 at += (int64_t)kThreads * Row<kDT>::kN) {
+                Row<kDT> g, v, d;
+                d.zero();
+                if (live) {
+                    g.load(gr, at, r.width);
+                    v.load(yr, at, r.width);
+#pragma unroll
+                    for (int i = 0; i < Row<kDT>::kN; ++i) {
+                        dot += g[i] * v[i];
+                        d.set(i, w * g[i]);
+                    }
+                }
+                d.store(to, at, r.width);
+            }
+        }
+#pragma unroll
+        for (int d = kWave / 2; d; d >>= 1) dot += __shfl_xor(dot, d);
+        if (threadIdx.x % kWave == 0) parts[threadIdx.x / kWave] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float sum = parts[0];
+#pragma unroll
+            for (int i = 1; i < kThreads / kWave; ++i) sum += parts[i];
+            weights_grad[token * r.top_k + j] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+int lanes_for(int64_t width, int values)
+{
+    int lanes = 16;
+    while (lanes < kThreads && (int64_t)lanes * values < width) lanes *= 2;
+    return lanes;
+}
+
+}  // namespace
+
+SortPlan expert_sort_plan(int64_t n)
+{
+    SortPlan s;
+    s.per_chunk = kChunkChoices;
+    if ((n + s.per_chunk - 1) / s.per_chunk > kMaxChunks)
+        s.per_chunk = ((n + kMaxChunks - 1) / kMaxChunks + kSortThreads - 1) / kSortThreads *
+                      kSortThreads;
+    s.chunks = (int)((n + s.per_chunk - 1) / s.per_chunk);
+    return s;
+}
+
+template <class Choice>
+static hipError_t sort_as(const void* choice, int64_t n, int experts, int32_t* order,
+                          int32_t* position, int32_t* offsets, int32_t* counts, int32_t* status,
+                          hipStream_t stream)
+{
+    const SortPlan s = expert_sort_plan(n);
+    const Choice* c = static_cast<const Choice*>(choice);
+    if (s.chunks > 1)
+        hipLaunchKernelGGL((expert_count_kernel<Choice>), dim3(s.chunks), dim3(kSortThreads), 0,
+                           stream, c, n, s.per_chunk, experts, counts);
+    const size_t lds = sizeof(int32_t) * (kSortWaves + 2) * (experts + 1);
+    hipLaunchKernelGGL((expert_place_kernel<Choice>), dim3(s.chunks), dim3(kSortThreads), lds,
+                       stream, c, n, s.per_chunk, experts, counts, order, position, offsets,
+                       status);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_sort(const void* choice, int choice_bytes, int64_t n, int experts,
+                              int32_t* order, int32_t* position, int32_t* offsets,
+                              int32_t* counts, int32_t* status, hipStream_t stream)
+{
+    if (n == 0) {
+        hipLaunchKernelGGL(no_choices_kernel, dim3(1), dim3(kThreads), 0, stream, offsets,
+                           experts + 1);
+        return hipGetLastError();
+    }
+    return choice_bytes == 8 ? sort_as<int64_t>(choice, n, experts, order, position, offsets,
+                                                counts, status, stream)
+                             : sort_as<int32_t>(choice, n, experts, order, position, offsets,
+                                                counts, status, stream);
+}
+
+hipError_t launch_expert_dispatch(int dtype, const Route& r, const void* x, int64_t ldx,
+                                  void* sorted, int64_t lds, hipStream_t stream)
+{
+    return with_dtype(dtype, [&](auto dt) {
+        constexpr int kDT = decltype(dt)::value;
+        const int lanes = lanes_for(r.width, Row<kDT>::kN);
+        const int64_t wgs = (r.tokens + kThreads / lanes - 1) / (kThreads / lanes);
+        hipLaunchKernelGGL((expert_dispatch_kernel<kDT>), dim3((unsigned)wgs), dim3(kThreads), 0,
+                           stream, r, x, ldx, sorted, lds, lanes);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_expert_combine(int dtype, const Route& r, const void* y, int64_t ldy,
+                                 const float* weights, void* out, int64_t ldo, hipStream_t stream)
+{
+    return with_dtype(dtype, [&](auto dt) {
+        constexpr int kDT = decltype(dt)::value;
+        const int lanes = lanes_for(r.width, Row<kDT>::kN);
+        const int64_t wgs = (r.tokens + kThreads / lanes - 1) / (kThreads / lanes);
+        if (weights)
+            hipLaunchKernelGGL((expert_combine_kernel<kDT, true>), dim3((unsigned)wgs),
+                               dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
+        else
+            hipLaunchKernelGGL((expert_combine_kernel<kDT, false>), dim3((unsigned)wgs),
+                               dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_expert_combine_backward(int dtype, const Route& r, const void* out_grad,
+                                          int64_t ldo, const void* y, int64_t ldy,
+                                          const float* weights, void* y_grad, int64_t ldg,
+                                          float* weights_grad, hipStream_t stream)
+{
+    return with_dtype(dtype, [&](auto dt) {
+        constexpr int kDT = decltype(dt)::value;
+        hipLaunchKernelGGL((expert_combine_backward_kernel<kDT>), dim3((unsigned)r.tokens),
+                           dim3(kThreads), 0, stream, r, out_grad, ldo, y, ldy, weights, y_grad,
+                           ldg, weights_grad);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace iqk

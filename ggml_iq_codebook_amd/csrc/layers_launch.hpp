@@ -1,0 +1,69 @@
+// layers_launch.hpp -- host-side launchers of the layer operators, called by
+// the entry points in api_layers.hip after argument validation.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace iqk {
+
+hipError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                                int8_t* q, int64_t ldq, float* scale, int32_t* status,
+                                hipStream_t stream);
+
+// An 8-bit product.  Dense: experts = 0, rows = tokens.  By expert: rows of y
+// in the order of their experts, the token of row p being order[p] / top_k
+// (p where order is null).
+struct Int8Product {
+    const int8_t* x;
+    int64_t ldx;
+    const float* x_scale;
+    const int8_t* w;
+    int64_t ldw;
+    int64_t w_stride;         // from one expert's weight to the next
+    const float* w_scale;
+    void* y;
+    int64_t ldy;
+    int64_t tokens;
+    int64_t rows;
+    int channels;
+    int depth;
+    int out_dtype;
+    const int32_t* order;
+    const int32_t* offsets;
+    int experts;
+    int top_k;
+};
+
+hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream);
+
+// Routing.  chunks: how many workgroups share the sort of n choices.
+struct SortPlan {
+    int chunks;
+    int64_t per_chunk;
+};
+SortPlan expert_sort_plan(int64_t n);
+hipError_t launch_expert_sort(const void* choice, int choice_bytes, int64_t n, int experts,
+                              int32_t* order, int32_t* position, int32_t* offsets,
+                              int32_t* counts, int32_t* status, hipStream_t stream);
+
+struct Route {
+    int64_t tokens;
+    int64_t width;
+    const int32_t* position;
+    int top_k;
+    const int32_t* kept;      // offsets + experts: the number of kept choices
+};
+
+hipError_t launch_expert_dispatch(int dtype, const Route& r, const void* x, int64_t ldx,
+                                  void* sorted, int64_t lds, hipStream_t stream);
+// weights null: all 1 (the gradient of dispatch).
+hipError_t launch_expert_combine(int dtype, const Route& r, const void* y, int64_t ldy,
+                                 const float* weights, void* out, int64_t ldo,
+                                 hipStream_t stream);
+hipError_t launch_expert_combine_backward(int dtype, const Route& r, const void* out_grad,
+                                          int64_t ldo, const void* y, int64_t ldy,
+                                          const float* weights, void* y_grad, int64_t ldg,
+                                          float* weights_grad, hipStream_t stream);
+
+}  // namespace iqk

@@ -85,7 +85,8 @@ typedef enum {
                                  an unknown weight dtype, a misaligned pointer */
     IQ_ERR_CODE = 9,          /* (device) a payload grid index beyond grid_size */
     IQ_ERR_HIP = 10,          /* a HIP runtime call or kernel launch failed */
-    IQ_ERR_DEVICE = 11        /* the current device is not a gfx950 GPU */
+    IQ_ERR_DEVICE = 11,       /* the current device is not a gfx950 GPU */
+    IQ_ERR_INDEX = 12         /* (device) an expert index outside -1..experts-1 (iq_layers.h) */
 } iq_status_t;
 
 typedef struct {

@@ -1,0 +1,184 @@
+"""CPU checks of the layer operators' C-ABI: every function that
+include/iq_layers.h declares is exported, workspaces are sized as stated, and
+bad arguments are refused before any device work."""
+
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "iq_layers.h")
+
+NULL, SHAPE, ARG, INDEX = 1, 3, 8, 12
+P = ctypes.c_void_p
+FAKE = P(0x100000)      # never dereferenced: validation fails before any device access
+ODD = P(0x100001)
+
+
+def declared_functions():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"^\s*(?:iq_status_t|int64_t)\s+(iq_\w+)\s*\(", text, flags=re.M)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import ggml_iq_codebook_amd as iq
+    return iq.load(build_if_missing=True)
+
+
+def test_library_exports_every_declared_symbol(lib):
+    assert declared_functions() == sorted([
+        "iq_quantize_rows", "iq_int8_matmul", "iq_int8_linear", "iq_int8_linear_workspace",
+        "iq_int8_expert_matmul", "iq_expert_sort", "iq_expert_sort_workspace", "iq_expert_dispatch",
+        "iq_expert_dispatch_backward", "iq_expert_combine", "iq_expert_combine_backward"])
+    for name in declared_functions():
+        assert hasattr(lib, name), name
+
+
+def test_status_of_a_bad_expert_has_a_name(lib):
+    import ggml_iq_codebook_amd as iq
+    assert lib.iq_status_str(INDEX) == b"expert index out of range"
+    assert iq.STATUS[INDEX] == "IQ_ERR_INDEX"
+
+
+def test_quantize_rows_refusals(lib):
+    f = lib.iq_quantize_rows
+    # dtype, x, ldx, rows, cols, q, ldq, scale, status, stream
+    assert f(0, None, 8, 1, 8, FAKE, 8, FAKE, FAKE, None) == NULL
+    assert f(0, FAKE, 8, 1, 8, None, 8, FAKE, FAKE, None) == NULL
+    assert f(0, FAKE, 8, 1, 8, FAKE, 8, None, FAKE, None) == NULL
+    assert f(0, FAKE, 8, -1, 8, FAKE, 8, FAKE, FAKE, None) == SHAPE
+    assert f(0, FAKE, 8, 1, 0, FAKE, 8, FAKE, FAKE, None) == SHAPE
+    assert f(0, FAKE, -8, 1, 8, FAKE, 8, FAKE, FAKE, None) == SHAPE
+    assert f(0, FAKE, 8, 2, 8, FAKE, 7, FAKE, FAKE, None) == SHAPE      # rows of q would overlap
+    assert f(0, FAKE, 8, 1 << 31, 8, FAKE, 8, FAKE, FAKE, None) == SHAPE
+    assert f(0, FAKE, 1 << 60, 1 << 20, 8, FAKE, 8, FAKE, FAKE, None) == SHAPE
+    assert f(3, FAKE, 8, 1, 8, FAKE, 8, FAKE, FAKE, None) == ARG        # fp64
+    assert f(-1, FAKE, 8, 1, 8, FAKE, 8, FAKE, FAKE, None) == ARG
+    assert f(0, P(0x100002), 8, 1, 8, FAKE, 8, FAKE, FAKE, None) == ARG
+    assert f(1, ODD, 8, 1, 8, FAKE, 8, FAKE, FAKE, None) == ARG
+    assert f(0, FAKE, 8, 1, 8, FAKE, 8, P(0x100002), FAKE, None) == ARG
+    assert f(0, FAKE, 8, 1, 8, FAKE, 8, FAKE, P(0x100002), None) == ARG
+    assert f(0, None, 8, 0, 8, None, 8, None, None, None) == 0          # nothing to do
+
+
+def test_int8_matmul_refusals(lib):
+    def f(x=FAKE, ldx=64, xs=FAKE, w=FAKE, ldw=64, ws=FAKE, t=4, n=8, k=64, dt=1, y=FAKE, ldy=8):
+        return lib.iq_int8_matmul(x, ldx, xs, w, ldw, ws, t, n, k, dt, y, ldy, None)
+    for name in ("x", "xs", "w", "ws", "y"):
+        assert f(**{name: None}) == NULL, name
+    for bad in (dict(t=-1), dict(n=0), dict(k=0), dict(k=131072), dict(ldx=-1), dict(ldw=-64),
+                dict(ldy=7), dict(t=1 << 31), dict(n=1 << 31), dict(ldx=1 << 60)):
+        assert f(**bad) == SHAPE, bad
+    for bad in (dict(dt=3), dict(dt=9), dict(y=ODD), dict(dt=0, y=P(0x100002)),
+                dict(xs=P(0x100002)), dict(ws=P(0x100002))):
+        assert f(**bad) == ARG, bad
+    assert f(t=0, x=None, xs=None, y=None) == 0
+
+
+def test_int8_linear_refusals(lib):
+    need = lib.iq_int8_linear_workspace(4, 70)
+    assert need == 4 * 80 + 16
+    assert lib.iq_int8_linear_workspace(0, 70) == 0
+    assert lib.iq_int8_linear_workspace(4, 0) == 0
+    assert lib.iq_int8_linear_workspace(4, 131072) == 0
+
+    def f(dt=1, x=FAKE, ldx=70, w=FAKE, ldw=70, ws=FAKE, t=4, n=8, k=70, y=FAKE, ldy=8, wk=FAKE,
+          wb=need, st=FAKE):
+        return lib.iq_int8_linear(dt, x, ldx, w, ldw, ws, t, n, k, y, ldy, wk, wb, st, None)
+    for name in ("x", "w", "ws", "y", "wk"):
+        assert f(**{name: None}) == NULL, name
+    for bad in (dict(t=-1), dict(n=0), dict(k=0), dict(k=131072), dict(ldy=7)):
+        assert f(**bad) == SHAPE, bad
+    for bad in (dict(dt=3), dict(x=ODD), dict(y=ODD), dict(wk=P(0x100008)), dict(wb=need - 1),
+                dict(st=P(0x100002)), dict(ws=P(0x100002))):
+        assert f(**bad) == ARG, bad
+    assert f(t=0, x=None, y=None, wk=None, wb=0) == 0
+
+
+def test_int8_expert_matmul_refusals(lib):
+    def f(x=FAKE, ldx=64, xs=FAKE, t=4, order=FAKE, k=2, off=FAKE, e=3, rows=8, w=FAKE, ldw=64,
+          wst=512, ws=FAKE, n=8, d=64, dt=1, y=FAKE, ldy=8):
+        return lib.iq_int8_expert_matmul(x, ldx, xs, t, order, k, off, e, rows, w, ldw, wst, ws, n,
+                                         d, dt, y, ldy, None)
+    for name in ("x", "xs", "off", "w", "ws", "y"):
+        assert f(**{name: None}) == NULL, name
+    for bad in (dict(t=-1), dict(t=0), dict(k=0), dict(e=0), dict(e=513), dict(rows=-1),
+                dict(rows=1 << 31), dict(wst=-1), dict(wst=1 << 60), dict(n=0), dict(d=0),
+                dict(d=131072), dict(ldy=7), dict(order=None)):          # 8 rows of 4 tokens
+        assert f(**bad) == SHAPE, bad
+    for bad in (dict(dt=3), dict(y=ODD), dict(order=P(0x100002)), dict(off=P(0x100002))):
+        assert f(**bad) == ARG, bad
+    assert f(rows=0, t=0, x=None, xs=None, y=None) == 0
+
+
+def test_expert_sort_refusals(lib):
+    assert lib.iq_expert_sort_workspace(4096, 16) == 0
+    assert lib.iq_expert_sort_workspace(4097, 16) == 2 * 17 * 4
+    assert lib.iq_expert_sort_workspace(2 ** 31 - 1, 512) <= 256 * 513 * 4
+    assert lib.iq_expert_sort_workspace(0, 16) == 0
+    assert lib.iq_expert_sort_workspace(4097, 513) == 0
+
+    def f(c=FAKE, cb=4, t=4, k=2, e=3, o=FAKE, p=FAKE, off=FAKE, wk=None, wb=0, st=FAKE):
+        return lib.iq_expert_sort(c, cb, t, k, e, o, p, off, wk, wb, st, None)
+    for name in ("c", "o", "p", "off"):
+        assert f(**{name: None}) == NULL, name
+    assert f(t=5000) == NULL                                             # needs a workspace
+    for bad in (dict(t=-1), dict(k=0), dict(e=0), dict(e=513), dict(t=1 << 30, k=2)):
+        assert f(**bad) == SHAPE, bad
+    for bad in (dict(cb=2), dict(cb=8, c=P(0x100004)), dict(c=P(0x100002)), dict(o=P(0x100002)),
+                dict(p=P(0x100002)), dict(off=P(0x100002)), dict(st=P(0x100002)),
+                dict(t=5000, wk=FAKE, wb=8), dict(t=5000, wk=P(0x100002), wb=1 << 20)):
+        assert f(**bad) == ARG, bad
+
+
+def test_routing_refusals(lib):
+    def dispatch(dt=1, a=FAKE, lda=16, t=4, d=16, p=FAKE, k=2, off=FAKE, e=3, b=FAKE, ldb=16):
+        return lib.iq_expert_dispatch(dt, a, lda, t, d, p, k, off, e, b, ldb, None)
+
+    def dispatch_backward(dt=1, a=FAKE, lda=16, t=4, d=16, p=FAKE, k=2, off=FAKE, e=3, b=FAKE, ldb=16):
+        return lib.iq_expert_dispatch_backward(dt, a, lda, t, d, p, k, off, e, b, ldb, None)
+
+    def combine(dt=1, a=FAKE, lda=16, t=4, d=16, p=FAKE, k=2, off=FAKE, e=3, b=FAKE, ldb=16, w=FAKE):
+        return lib.iq_expert_combine(dt, a, lda, t, d, p, k, off, e, w, b, ldb, None)
+
+    def combine_backward(dt=1, a=FAKE, lda=16, t=4, d=16, p=FAKE, k=2, off=FAKE, e=3, b=FAKE, ldb=16,
+                         w=FAKE, g=FAKE, ldg=16, gw=FAKE):
+        return lib.iq_expert_combine_backward(dt, g, ldg, a, lda, t, d, p, k, off, e, w, b, ldb, gw, None)
+
+    more = {dispatch: (), dispatch_backward: (), combine: ("w",), combine_backward: ("w", "g", "gw")}
+    for f, names in more.items():
+        for name in ("a", "p", "off", "b") + names:
+            assert f(**{name: None}) == NULL, (f, name)
+        for bad in (dict(t=-1), dict(d=0), dict(k=0), dict(e=0), dict(e=513), dict(lda=-1),
+                    dict(ldb=15), dict(t=1 << 30, k=2), dict(t=(1 << 62), k=4), dict(d=1 << 62, ldb=1 << 62)):
+            assert f(**bad) == SHAPE, (f, bad)
+        for bad in (dict(dt=3), dict(dt=7), dict(a=ODD), dict(b=ODD), dict(p=P(0x100002)),
+                    dict(off=P(0x100002))):
+            assert f(**bad) == ARG, (f, bad)
+        assert f(t=0, a=None, b=None, p=None, off=None) == 0
+    assert combine(w=P(0x100002)) == ARG
+    assert combine_backward(g=ODD) == ARG
+    assert combine_backward(gw=P(0x100002)) == ARG
+
+
+def test_binding_refuses_cpu_tensors():
+    import torch
+
+    import ggml_iq_codebook_amd as iq
+    x = torch.zeros((2, 4))
+    q = torch.zeros((2, 4), dtype=torch.int8)
+    s = torch.zeros(2)
+    place = torch.zeros((2, 1), dtype=torch.int32)
+    off = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: iq.quantize_rows(x), lambda: iq.int8_matmul(q, s, q, s),
+                 lambda: iq.int8_linear(x, q, s),
+                 lambda: iq.int8_expert_matmul(q, s, q[None], s[None], off),
+                 lambda: iq.expert_sort(place, 1), lambda: iq.expert_dispatch(x, place, off),
+                 lambda: iq.expert_dispatch_backward(x, place, off),
+                 lambda: iq.expert_combine(x, place, off, s[:, None]),
+                 lambda: iq.expert_combine_backward(x, x, place, off, s[:, None])):
+        with pytest.raises(ValueError):
+            call()
