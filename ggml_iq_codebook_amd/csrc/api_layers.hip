@@ -125,7 +125,9 @@ iq_status_t iq_int8_matmul(const int8_t* x, int64_t ldx, const float* x_scale, c
 
 int64_t iq_int8_linear_workspace(int64_t tokens, int64_t depth)
 {
-    if (tokens < 1 || tokens > INT32_MAX || depth < 1 || depth > IQ_MAX_INT8_DEPTH) return 0;
+    if (tokens < 1 || tokens > INT32_MAX || depth < 1 || depth > IQ_MAX_INT8_DEPTH ||
+        iqk::int8_decode_takes(tokens, depth))
+        return 0;
     return tokens * code_stride(depth) + round_up(tokens * 4, 16);
 }
 
@@ -147,12 +149,14 @@ iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const i
     if (st) return st;
     int8_t* codes = static_cast<int8_t*>(workspace);
     const int64_t ldc = code_stride(depth);
-    float* scale = reinterpret_cast<float*>(codes + tokens * ldc);
+    float* scale = codes ? reinterpret_cast<float*>(codes + tokens * ldc) : nullptr;
     const iqk::Int8Product p = {codes,  ldc,    scale,   w,       ldw,
                                 0,      w_scale, y,      ldy,     tokens,
                                 tokens, (int)channels,   (int)depth, (int)dtype,
                                 nullptr, nullptr, 0,     1};
     return run_with_status(status, stream, [&](int32_t* s) {
+        if (iqk::int8_decode_takes(tokens, depth))
+            return iqk::launch_int8_decode(p, dtype, x, ldx, s, stream);
         const hipError_t e = iqk::launch_quantize_rows(dtype, x, ldx, tokens, depth, codes, ldc,
                                                        scale, s, stream);
         return e != hipSuccess ? e : iqk::launch_int8_product(p, cus, stream);

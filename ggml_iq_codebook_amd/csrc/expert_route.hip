@@ -179,52 +179,7 @@ __global__ void no_choices_kernel(int32_t* offsets, int keys)
 
 constexpr int kThreads = 256;
 
-// A row is shared by `lanes` threads (a power of two), 16 bytes a lane.  The
-// addresses need the alignment of a value only (global memory instructions
-// take any address; memcpy tells the compiler); the last vector of a row whose
-// width is no multiple goes value by value.
-template <int kDT>
-struct Row {
-    typedef typename Value<kDT>::raw raw;
-    static constexpr int kN = 16 / (int)sizeof(raw);
-    uint32_t u[4];
-    __device__ __forceinline__ raw get(int i) const
-    {
-        return sizeof(raw) == 4 ? (raw)u[i] : (raw)(u[i / 2] >> (16 * (i % 2)));
-    }
-    __device__ __forceinline__ void load(const raw* row, int64_t at, int64_t width)
-    {
-        if (at + kN <= width) {
-            __builtin_memcpy(u, row + at, 16);
-        } else {
-            zero();
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                if (at + i < width) put(i, row[at + i]);
-        }
-    }
-    __device__ __forceinline__ void store(raw* row, int64_t at, int64_t width) const
-    {
-        if (at + kN <= width) {
-            __builtin_memcpy(row + at, u, 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                if (at + i < width) row[at + i] = get(i);
-        }
-    }
-    __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0u; }
-    // Value i of a vector that held 0 there.
-    __device__ __forceinline__ void put(int i, raw r)
-    {
-        if (sizeof(raw) == 4)
-            u[i] = r;
-        else
-            u[i / 2] |= (uint32_t)r << (16 * (i % 2));
-    }
-    __device__ __forceinline__ float operator[](int i) const { return Value<kDT>::load(get(i)); }
-    __device__ __forceinline__ void set(int i, float f) { put(i, Value<kDT>::store(f)); }
-};
+// A row is shared by `lanes` threads (a power of two), 16 bytes a lane.
 
 // The place of a token's choice: -1 outside the sorted rows (skipped).
 __device__ __forceinline__ int64_t place_of(const Route& r, int64_t token, int j)
@@ -262,7 +217,8 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
     }
 }
 
-// kWeighted: combine; otherwise the gradient of dispatch.
+// kWeighted: combine; otherwise the gradient of dispatch.  The rows of kGroup
+// choices are on their way at once; the sum keeps the order of the choices.
 template <int kDT, bool kWeighted>
 __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
                                                                   const void* __restrict__ y,
@@ -272,6 +228,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
                                                                   int64_t ldo, int lanes)
 {
     typedef typename Value<kDT>::raw raw;
+    constexpr int kGroup = 4;
     const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
     if (token >= r.tokens) return;
     const int64_t kept = *r.kept;
@@ -279,14 +236,35 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
     for (int64_t at = (int64_t)(threadIdx.x % lanes) * Row<kDT>::kN; at < r.width;
          at += (int64_t)lanes * Row<kDT>::kN) {
         float sum[Row<kDT>::kN] = {};
-        for (int j = 0; j < r.top_k; ++j) {
-            const int64_t p = place_of(r, token, j);
-            if (p < 0 || p >= kept) continue;
-            Row<kDT> v;
-            v.load(static_cast<const raw*>(y) + p * ldy, at, r.width);
-            const float w = kWeighted ? weights[token * r.top_k + j] : 1.0f;
+        for (int j0 = 0; j0 < r.top_k; j0 += kGroup) {
+            // Rows that do not count are replaced by row 0, which is there, and
+            // left out of the sum: no branch keeps the loads apart.
+            Row<kDT> v[kGroup];
+            float w[kGroup];
+            bool live[kGroup];
+            const raw* from[kGroup];
 #pragma unroll
-            for (int i = 0; i < Row<kDT>::kN; ++i) sum[i] += kWeighted ? w * v[i] : v[i];
+            for (int g = 0; g < kGroup; ++g) {
+                const int j = min(j0 + g, r.top_k - 1);
+                const int64_t p = place_of(r, token, j);
+                live[g] = j0 + g < r.top_k && p >= 0 && p < kept;
+                w[g] = kWeighted ? weights[token * r.top_k + j] : 1.0f;
+                from[g] = static_cast<const raw*>(y) + (live[g] ? p : 0) * ldy;
+            }
+            if (at + Row<kDT>::kN <= r.width) {
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) __builtin_memcpy(v[g].u, from[g] + at, 16);
+            } else {
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) v[g].load(from[g], at, r.width);
+            }
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g)
+#pragma unroll
+                for (int i = 0; i < Row<kDT>::kN; ++i) {
+                    const float term = kWeighted ? w[g] * v[g][i] : v[g][i];
+                    sum[i] = live[g] ? sum[i] + term : sum[i];
+                }
         }
         Row<kDT> o;
         o.zero();

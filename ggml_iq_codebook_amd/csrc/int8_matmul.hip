@@ -4,8 +4,8 @@
 //
 // The sums are exact in 32-bit integers, so neither tiling nor the order of the
 // depth changes a result.  Both operands hold their depth innermost, which is
-// how the matrix instructions take it: lane l of v_mfma_i32_32x32x32_i8
-// supplies row l%32, depth 16*(l/32)..+15, as one 16-byte register group.
+// how the matrix instructions take it: lane l of v_mfma_i32_16x16x64_i8
+// supplies row l%16, depth 16*(l/16)..+15, as one 16-byte register group.
 // The weight is the first operand, so a lane's results are 4 consecutive
 // channels of one token and go out as one store.
 #include <hip/hip_runtime.h>
@@ -18,9 +18,6 @@ namespace iqk {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
-
-constexpr int kDepth = 128;           // bytes of a row in a staged tile
 
 // ---------------------------------------------------------------------------
 // Which rows a tile works on
@@ -203,23 +200,48 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* row, int at, int depth
     return v;
 }
 
+// A staged row of kDepth bytes is stored in pieces of 16, piece c in slot
+// c ^ swizzle(row): eight lanes that read one piece of consecutive rows meet
+// eight different groups of banks.
+template <int kDepth>
+__device__ __forceinline__ int swizzle(int row)
+{
+    return kDepth == 64 ? (row >> 1) & 3 : (kDepth == 128 ? row & 7 : row & 15);
+}
+
+// Waits until at most kLeft of this wave's loads are under way and all its LDS
+// reads have arrived, then for the other waves.
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+
 // kWT x kWC waves share a tile of kRows rows of y by kChannels channels, each
-// a part of kRows/kWT by kChannels/kWC, in steps of 128 of the depth.  The
-// tiles of both operands are double buffered in LDS: the next step is on its
-// way while this one is multiplied.  A row of 128 bytes is stored as 8 pieces
-// of 16, piece c in slot c ^ (row % 8), so that lanes reading one piece of
-// consecutive rows meet different banks.  kDirect: rows start on 16 bytes and
-// the depth is a multiple of 16, and the pieces go straight into LDS;
-// otherwise they pass through registers, with the ends of rows cut byte by byte.
-template <int kRows, int kChannels, int kWT, int kWC, bool kDirect, bool kExperts>
-__global__ __launch_bounds__(kWT* kWC* kWave) void int8_tile_kernel(Int8Product p,
-                                                                    int channel_tiles)
+// a part of kRows/kWT by kChannels/kWC, in steps of kDepth of the depth.  The
+// tiles of both operands go through a ring of kStages buffers in LDS.
+//
+// kDirect: rows start on 16 bytes, and pieces are copied straight into LDS,
+// kStages - 1 steps ahead.  Otherwise they pass through registers, kAhead
+// steps ahead, with the ends of rows cut byte by byte, into two buffers.
+//
+// kPingPong (8 waves, two on a SIMD): the second four waves run half a step
+// behind, so on each SIMD one wave multiplies while the other reads its
+// operands; a step is two barriers long.
+template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,
+          bool kDirect, bool kExperts>
+__global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kernel(Int8Product p,
+                                                                                 int channel_tiles)
 {
     constexpr int kWaves = kWT * kWC, kThreads = kWaves * kWave;
-    constexpr int kFT = kRows / kWT / 32, kFC = kChannels / kWC / 32;
-    constexpr int kLoads = (kRows + kChannels) / 8 / kWaves;   // a wave's, 8 rows each
-    static_assert((kRows + kChannels) % (8 * kWaves) == 0 && kChannels % 8 == 0, "tile");
-    __shared__ __align__(1024) int8_t staged[2][(kRows + kChannels) * kDepth];
+    constexpr int kFT = kRows / kWT / 16, kFC = kChannels / kWC / 16;
+    constexpr int kPieces = kDepth / 16;
+    constexpr int kRowsPerLoad = kWave / kPieces;
+    constexpr int kLoads = (kRows + kChannels) / kRowsPerLoad / kWaves;   // a wave's
+    constexpr int kBuffers = kDirect ? kStages : 2;
+    constexpr int kAhead = 2;
+    static_assert(kLoads * kRowsPerLoad * kWaves == kRows + kChannels && kFT > 0 && kFC > 0, "tile");
+    __shared__ __align__(1024) int8_t staged[kBuffers][(kRows + kChannels) * kDepth];
 
     const Tile t = kExperts ? expert_tile<kRows>(p, channel_tiles)
                             : dense_tile<kRows>(p, channel_tiles);
@@ -239,8 +261,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave) void int8_tile_kernel(Int8Product 
     int piece[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int r = (wave * kLoads + i) * 8 + lane / 8;
-        piece[i] = ((lane % 8) ^ (r % 8)) * 16;
+        const int r = (wave * kLoads + i) * kRowsPerLoad + lane / kPieces;
+        piece[i] = ((lane % kPieces) ^ swizzle<kDepth>(r)) * 16;
         if (r < kChannels) {
             from[i] = w + (int64_t)min(channel0 + r, p.channels - 1) * p.ldw;
         } else {
@@ -248,93 +270,179 @@ __global__ __launch_bounds__(kWT* kWC* kWave) void int8_tile_kernel(Int8Product 
             from[i] = p.x + (kExperts ? token_of(p, row) : row) * p.ldx;
         }
     }
+    const int steps = (p.depth + kDepth - 1) / kDepth;
+    // Steps before this one lie within the rows.
+    const int whole = p.depth / kDepth;
 
-    uint4 passing[kDirect ? 1 : kLoads];
-    auto fetch = [&](int b, int step) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = step * kDepth + piece[i];
-            if constexpr (kDirect)
-                copy_to_lds(at < p.depth ? from[i] + at : reinterpret_cast<const int8_t*>(zeros),
-                            &staged[b][(wave * kLoads + i) * 1024]);
-            else
-                passing[i] = load_codes(from[i], at, p.depth);
-        }
-    };
-    auto arrive = [&](int b) {
-        if constexpr (!kDirect) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                *reinterpret_cast<uint4*>(&staged[b][(wave * kLoads + i) * 1024 + lane * 16]) =
-                    passing[i];
-        }
-    };
-
-    v16i acc[kFC][kFT] = {};
+    v4i acc[kFC][kFT] = {};
     const int wt = wave % kWT, wc = wave / kWT;
-    const int row_c = wc * kFC * 32 + lane % 32;
-    const int row_t = kChannels + wt * kFT * 32 + lane % 32;
-    const int half = lane / 32;
-    auto multiply = [&](int b) {
+    const int row_c = wc * kFC * 16 + lane % 16;
+    const int row_t = kChannels + wt * kFT * 16 + lane % 16;
+    const int quarter = lane / 16;
+    constexpr int kParts = kDepth / 64;
+    auto read = [&](int b, int k, v4i (&a)[kFC], v4i (&x)[kFT]) {
 #pragma unroll
-        for (int k = 0; k < kDepth / 32; ++k) {
-            v4i a[kFC], x[kFT];
+        for (int i = 0; i < kFC; ++i)
+            a[i] = *reinterpret_cast<const v4i*>(
+                &staged[b][(row_c + i * 16) * kDepth +
+                           ((4 * k + quarter) ^ swizzle<kDepth>(row_c)) * 16]);
 #pragma unroll
-            for (int i = 0; i < kFC; ++i)
-                a[i] = *reinterpret_cast<const v4i*>(
-                    &staged[b][(row_c + i * 32) * kDepth + ((2 * k + half) ^ (row_c % 8)) * 16]);
+        for (int j = 0; j < kFT; ++j)
+            x[j] = *reinterpret_cast<const v4i*>(
+                &staged[b][(row_t + j * 16) * kDepth +
+                           ((4 * k + quarter) ^ swizzle<kDepth>(row_t)) * 16]);
+    };
+    auto multiply = [&](const v4i (&a)[kFC], const v4i (&x)[kFT]) {
+#pragma unroll
+        for (int i = 0; i < kFC; ++i)
 #pragma unroll
             for (int j = 0; j < kFT; ++j)
-                x[j] = *reinterpret_cast<const v4i*>(
-                    &staged[b][(row_t + j * 32) * kDepth + ((2 * k + half) ^ (row_t % 8)) * 16]);
-#pragma unroll
-            for (int i = 0; i < kFC; ++i)
-#pragma unroll
-                for (int j = 0; j < kFT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], x[j], acc[i][j], 0, 0, 0);
-        }
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], x[j], acc[i][j], 0, 0, 0);
     };
 
-    const int steps = (p.depth + kDepth - 1) / kDepth;
-    fetch(0, 0);
-    arrive(0);
-    __syncthreads();
-    for (int s = 0; s < steps; s += 2) {
-        if (s + 1 < steps) fetch(1, s + 1);
-        multiply(0);
-        if (s + 1 < steps) arrive(1);
-        __syncthreads();
-        if (s + 1 >= steps) break;
-        if (s + 2 < steps) fetch(0, s + 2);
-        multiply(1);
-        if (s + 2 < steps) arrive(0);
-        __syncthreads();
+    if constexpr (kDirect) {
+        auto fetch = [&](int b, int step) {
+            if (step < whole) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    copy_to_lds(from[i] + (int64_t)step * kDepth + piece[i],
+                                &staged[b][(wave * kLoads + i) * 1024]);
+            } else {
+                // The end of the rows: pieces beyond it are zeros, and the piece
+                // that holds it is cut in registers.
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int at = step * kDepth + piece[i];
+                    copy_to_lds(at + 16 <= p.depth ? from[i] + at
+                                                   : reinterpret_cast<const int8_t*>(zeros),
+                                &staged[b][(wave * kLoads + i) * 1024]);
+                }
+                if (p.depth % 16) {
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int at = step * kDepth + piece[i];
+                        if (at < p.depth && at + 16 > p.depth)
+                            *reinterpret_cast<uint4*>(
+                                &staged[b][(wave * kLoads + i) * 1024 + lane * 16]) =
+                                load_codes(from[i], at, p.depth);
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                }
+            }
+        };
+        constexpr int kLeft = (kStages - 2) * kLoads;
+        static_assert(kLeft < 64, "vmcnt holds 6 bits");
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            if (i < steps) fetch(i, i);
+        if constexpr (kPingPong) {
+            const bool late = wave >= kWaves / 2;
+            if (steps >= kStages - 1)
+                wait_and_meet<kLeft>();
+            else
+                wait_and_meet<0>();
+            if (late) asm volatile("s_barrier" ::: "memory");
+            for (int s0 = 0; s0 < steps; s0 += kStages) {
+#pragma unroll
+                for (int u = 0; u < kStages; ++u) {
+                    const int s = s0 + u;
+                    if (s >= steps) break;
+                    v4i a[kParts][kFC], x[kParts][kFT];
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) read(u, k, a[k], x[k]);
+                    // The buffer of step s - 1: both halves read it before the
+                    // last barrier.  Step s + 1 has to be there for the next.
+                    if (s + kStages - 1 < steps) {
+                        fetch((u + kStages - 1) % kStages, s + kStages - 1);
+                        wait_and_meet<kLeft>();
+                    } else {
+                        wait_and_meet<0>();
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) multiply(a[k], x[k]);
+                    __builtin_amdgcn_s_setprio(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    asm volatile("s_barrier" ::: "memory");
+                }
+            }
+            if (!late) asm volatile("s_barrier" ::: "memory");
+        } else {
+            for (int s0 = 0; s0 < steps; s0 += kStages) {
+#pragma unroll
+                for (int u = 0; u < kStages; ++u) {
+                    const int s = s0 + u;
+                    if (s >= steps) break;
+                    if (s + kStages - 2 < steps)
+                        wait_and_meet<kLeft>();
+                    else
+                        wait_and_meet<0>();
+                    if (s + kStages - 1 < steps)
+                        fetch((u + kStages - 1) % kStages, s + kStages - 1);
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) {
+                        v4i a[kFC], x[kFT];
+                        read(u, k, a, x);
+                        multiply(a, x);
+                    }
+                }
+            }
+        }
+    } else {
+        uint4 passing[kAhead][kLoads];
+        auto fetch = [&](int set, int step) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                passing[set][i] = load_codes(from[i], step * kDepth + piece[i], p.depth);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i, i);
+        for (int s0 = 0; s0 < steps; s0 += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int s = s0 + u;
+                if (s >= steps) break;
+                // Buffer u was last read in step s - 2, before the last barrier.
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    *reinterpret_cast<uint4*>(&staged[u][(wave * kLoads + i) * 1024 + lane * 16]) =
+                        passing[u][i];
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                fetch(u, s + kAhead);
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    v4i a[kFC], x[kFT];
+                    read(u, k, a, x);
+                    multiply(a, x);
+                }
+            }
+        }
     }
 
 #pragma unroll
     for (int j = 0; j < kFT; ++j) {
-        const int64_t row = t.row0 + wt * kFT * 32 + j * 32 + lane % 32;
+        const int64_t row = t.row0 + (wt * kFT + j) * 16 + lane % 16;
         if (row >= t.row_end) continue;
         const float sx = p.x_scale[kExperts ? token_of(p, row) : row];
         const float* sw = p.w_scale + (int64_t)t.expert * p.channels;
 #pragma unroll
-        for (int i = 0; i < kFC; ++i)
+        for (int i = 0; i < kFC; ++i) {
+            const int channel = channel0 + (wc * kFC + i) * 16 + 4 * quarter;
+            if (channel >= p.channels) continue;
+            float f[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int channel = channel0 + wc * kFC * 32 + i * 32 + 8 * g + 4 * half;
-                if (channel >= p.channels) continue;
-                float f[4];
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    f[v] = (float)acc[i][j][4 * g + v] * sx *
-                           sw[min(channel + v, p.channels - 1)];
-                store4(p, row, channel, f);
-            }
+            for (int v = 0; v < 4; ++v)
+                f[v] = (float)acc[i][j][v] * sx * sw[min(channel + v, p.channels - 1)];
+            store4(p, row, channel, f);
+        }
     }
 }
 
-template <int kRows, int kChannels, int kWT, int kWC>
-hipError_t launch_tiles(const Int8Product& p, bool direct, hipStream_t stream)
+template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,
+          bool kDirect>
+hipError_t launch_tiles(const Int8Product& p, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
     // Every expert (and the dropped rows) may end in a tile that is not full.
@@ -343,33 +451,57 @@ hipError_t launch_tiles(const Int8Product& p, bool direct, hipStream_t stream)
     const int64_t wgs = row_tiles * channel_tiles;
     if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)wgs), threads(kWT * kWC * kWave);
-    if (p.experts) {
-        if (direct)
-            hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, true, true>), grid,
-                               threads, 0, stream, p, channel_tiles);
-        else
-            hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, false, true>), grid,
-                               threads, 0, stream, p, channel_tiles);
-    } else {
-        if (direct)
-            hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, true, false>), grid,
-                               threads, 0, stream, p, channel_tiles);
-        else
-            hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, false, false>), grid,
-                               threads, 0, stream, p, channel_tiles);
-    }
+    if (p.experts)
+        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kDepth, kStages,
+                                             kPingPong, kDirect, true>),
+                           grid, threads, 0, stream, p, channel_tiles);
+    else
+        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kDepth, kStages,
+                                             kPingPong, kDirect, false>),
+                           grid, threads, 0, stream, p, channel_tiles);
     return hipGetLastError();
+}
+
+// The expected time of a tile size, in units of a step over 4096 of the depth:
+// every compute unit takes its tiles one after another, or two at once where
+// two fit its LDS.  one, two: measured microseconds of one tile and of two at
+// once, at a depth of 4096.
+double tile_cost(const Int8Product& p, int cus, int rows, int channels, double one, double two)
+{
+    double row_tiles = (double)((p.rows + rows - 1) / rows);
+    if (p.experts) {
+        // Rows spread over the experts: each that has any ends in half a tile.
+        const double used = p.rows < p.experts ? (double)p.rows : (double)p.experts;
+        row_tiles = (double)p.rows / rows + 0.5 * used;
+        if (row_tiles < used) row_tiles = used;
+    }
+    const double tiles = row_tiles * (double)((p.channels + channels - 1) / channels);
+    const int64_t each = (int64_t)((tiles + cus - 1) / cus);
+    return two > 0.0 ? (double)(each / 2) * two + (double)(each % 2) * one : (double)each * one;
 }
 
 }  // namespace
 
+// Which tile: the one with the least expected time.
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream)
 {
-    const bool direct = p.depth % 16 == 0 && p.ldx % 16 == 0 && p.ldw % 16 == 0 &&
-                        p.w_stride % 16 == 0 && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
+    const bool direct = p.ldx % 16 == 0 && p.ldw % 16 == 0 && p.w_stride % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
-    (void)cus;
-    return launch_tiles<128, 128, 2, 2>(p, direct, stream);
+    const double t32 = tile_cost(p, cus, 32, 32, 5.5, 8.2);
+    const double t64 = tile_cost(p, cus, 64, 64, 9.3, 14.0);
+    const double t128 = tile_cost(p, cus, 128, 128, 17.0, 0.0);
+    const double t256 = tile_cost(p, cus, 256, 256, 48.0, 0.0);
+    if (!direct) {
+        if (t32 <= t64 && t32 <= t128) return launch_tiles<32, 32, 2, 2, 256, 2, false, false>(p, stream);
+        if (t64 <= t128) return launch_tiles<64, 64, 2, 2, 128, 2, false, false>(p, stream);
+        return launch_tiles<128, 128, 2, 2, 128, 2, false, false>(p, stream);
+    }
+    if (t32 <= t64 && t32 <= t128 && t32 <= t256)
+        return launch_tiles<32, 32, 2, 2, 256, 4, false, true>(p, stream);
+    if (t64 <= t128 && t64 <= t256) return launch_tiles<64, 64, 2, 2, 128, 4, false, true>(p, stream);
+    if (t128 <= t256) return launch_tiles<128, 128, 4, 2, 128, 4, true, true>(p, stream);
+    return launch_tiles<256, 256, 4, 2, 64, 4, true, true>(p, stream);
 }
 
 }  // namespace iqk

@@ -41,14 +41,51 @@ struct Value<IQ_DTYPE_F16> {
     }
 };
 
-// n consecutive values read or written as one or two instructions.  The
-// addresses need the alignment of the value only: global memory instructions
-// take any address, and the compiler is told so by going through memcpy.
-template <class T, int kN>
-struct Pack {
-    T v[kN];
-    __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, p, sizeof(v)); }
-    __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, v, sizeof(v)); }
+// 16 bytes of a row, read or written as one instruction.  The addresses need
+// the alignment of a value only (global memory instructions take any address;
+// memcpy tells the compiler).  The last vector of a row whose width is no
+// multiple goes value by value, and values beyond the width read as 0.
+template <int kDT>
+struct Row {
+    typedef typename Value<kDT>::raw raw;
+    static constexpr int kN = 16 / (int)sizeof(raw);
+    uint32_t u[4];
+    __device__ __forceinline__ raw get(int i) const
+    {
+        return sizeof(raw) == 4 ? (raw)u[i] : (raw)(u[i / 2] >> (16 * (i % 2)));
+    }
+    __device__ __forceinline__ void load(const raw* row, int64_t at, int64_t width)
+    {
+        if (at + kN <= width) {
+            __builtin_memcpy(u, row + at, 16);
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (at + i < width) put(i, row[at + i]);
+        }
+    }
+    __device__ __forceinline__ void store(raw* row, int64_t at, int64_t width) const
+    {
+        if (at + kN <= width) {
+            __builtin_memcpy(row + at, u, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (at + i < width) row[at + i] = get(i);
+        }
+    }
+    __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0u; }
+    // Value i of a vector that held 0 there.
+    __device__ __forceinline__ void put(int i, raw r)
+    {
+        if (sizeof(raw) == 4)
+            u[i] = r;
+        else
+            u[i / 2] |= (uint32_t)r << (16 * (i % 2));
+    }
+    __device__ __forceinline__ float operator[](int i) const { return Value<kDT>::load(get(i)); }
+    __device__ __forceinline__ void set(int i, float f) { put(i, Value<kDT>::store(f)); }
 };
 
 // Runs body(kDT constant) for a validated storage type.

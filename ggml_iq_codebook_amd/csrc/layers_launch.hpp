@@ -37,6 +37,22 @@ struct Int8Product {
 
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream);
 
+// The layer for a few tokens, rounding included, as one launch.  Its tokens are
+// dealt out in parts of 512 values of which a workgroup keeps kDecodeParts.
+constexpr int kDecodeParts = 32;
+__host__ __device__ constexpr int decode_stride(int depth)
+{
+    // Whole pieces of 64, and rows that start on different banks.
+    return (depth + 63) / 64 * 64 + 16;
+}
+inline bool int8_decode_takes(int64_t tokens, int64_t depth)
+{
+    return tokens <= 16 && tokens * ((depth + 511) / 512) <= kDecodeParts;
+}
+// p.x, p.x_scale are not used; y has the type of x.
+hipError_t launch_int8_decode(const Int8Product& p, int dtype, const void* x, int64_t ldx,
+                              int32_t* status, hipStream_t stream);
+
 // Routing.  chunks: how many workgroups share the sort of n choices.
 struct SortPlan {
     int chunks;

@@ -3,64 +3,35 @@
 // reciprocal and the product rounded to nearest, the division correctly rounded.
 //
 // Bound by HBM: a row is read once, kept in registers while its maximum is
-// found, and written as one byte per value.  The maximum is taken over the
-// bits of |x| as integers, which also orders infinities and NaN above every
-// finite value, so one comparison finds a row that has to be refused.
+// found, and written as one byte per value.
 #include <hip/hip_runtime.h>
 
-#include "layers_common.hpp"
 #include "layers_launch.hpp"
+#include "row_codes.hpp"
 
 namespace iqk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8;             // values a lane reads and writes at once
 
-template <int kDT>
-__device__ __forceinline__ uint32_t load_chunk(const typename Value<kDT>::raw* row, int64_t at,
-                                               int64_t cols, float (&v)[kChunk])
-{
-    typedef typename Value<kDT>::raw raw;
-    Pack<raw, kChunk> p;
-    if (at + kChunk <= cols) {
-        p.load(row + at);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) p.v[i] = at + i < cols ? row[at + i] : raw(0);
-    }
-    uint32_t top = 0u;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        v[i] = Value<kDT>::load(p.v[i]);
-        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    }
-    return top;
-}
-
+template <int kDT, bool kWhole>
 __device__ __forceinline__ void store_chunk(int8_t* row, int64_t at, int64_t cols,
-                                            const float (&v)[kChunk], float scale)
+                                            const Chunk<kDT, kWhole>& v, float scale, float inv)
 {
-    Pack<int8_t, kChunk> q;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        // |x| / scale rounds to 127 at most, but for scales among the smallest
-        // subnormals, whose own rounding is coarse.
-        const float r = scale > 0.0f ? rintf(v[i] / scale) : 0.0f;
-        q.v[i] = (int8_t)fminf(fmaxf(r, -127.0f), 127.0f);
-    }
-    if (at + kChunk <= cols) {
-        q.store(row + at);
+    uint32_t b[kChunk / 4];
+    codes_of(v, scale, inv, b);
+    if (kWhole || at + kChunk <= cols) {
+        __builtin_memcpy(row + at, b, kChunk);
     } else {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
-            if (at + i < cols) row[at + i] = q.v[i];
+            if (at + i < cols) row[at + i] = (int8_t)(b[i / 4] >> (8 * (i % 4)));
     }
 }
 
 // kLanes lanes share a row (64: a wave; 256: the workgroup); each keeps kKeep
 // chunks of it in registers, and rows longer than that are read again.
-template <int kDT, int kLanes, int kKeep>
+template <int kDT, int kLanes, int kKeep, bool kWhole>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     const void* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, int8_t* __restrict__ q,
     int64_t ldq, float* __restrict__ scales, int32_t* status)
@@ -74,15 +45,17 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     const raw* xr = static_cast<const raw*>(x) + row * ldx;
     int8_t* qr = q + row * ldq;
 
-    float v[kKeep][kChunk];
+    Chunk<kDT, kWhole> kept[kKeep];
     uint32_t top = 0u;
 #pragma unroll
-    for (int c = 0; c < kKeep; ++c)
-        top = max(top, load_chunk<kDT>(xr, ((int64_t)c * kLanes + lane) * kChunk, cols, v[c]));
+    for (int c = 0; c < kKeep; ++c) kept[c].load(xr, (c * kLanes + lane) * kChunk, cols);
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c) top = max(top, kept[c].top());
     constexpr int64_t kKept = (int64_t)kKeep * kLanes * kChunk;
     for (int64_t at = kKept + lane * kChunk; at < cols; at += kLanes * kChunk) {
-        float u[kChunk];
-        top = max(top, load_chunk<kDT>(xr, at, cols, u));
+        Chunk<kDT, kWhole> u;
+        u.load(xr, at, cols);
+        top = max(top, u.top());
     }
 #pragma unroll
     for (int d = kWave / 2; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -93,21 +66,26 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
         for (int i = 0; i < kThreads / kWave; ++i) top = max(top, tops[i]);
     }
 
-    const bool finite = top < 0x7f800000u;
-    const float scale = finite ? __uint_as_float(top) * (1.0f / 127.0f) : 0.0f;
+    const float scale = row_scale(top);
     if (lane == 0) {
         scales[row] = scale;
-        if (!finite) report_generic(status, IQ_ERR_NONFINITE);
+        if (top >= 0x7f800000u) report_generic(status, IQ_ERR_NONFINITE);
     }
+    if (!(scale > 0.0f)) {
+        // A row of zeros, or one that is refused.
+        for (int64_t at = lane; at < cols; at += kLanes) qr[at] = 0;
+        return;
+    }
+    const float inv = 1.0f / scale;
 #pragma unroll
     for (int c = 0; c < kKeep; ++c) {
-        const int64_t at = ((int64_t)c * kLanes + lane) * kChunk;
-        if (at < cols) store_chunk(qr, at, cols, v[c], scale);
+        const int64_t at = (c * kLanes + lane) * kChunk;
+        if (at < cols) store_chunk(qr, at, cols, kept[c], scale, inv);
     }
     for (int64_t at = kKept + lane * kChunk; at < cols; at += kLanes * kChunk) {
-        float u[kChunk];
-        load_chunk<kDT>(xr, at, cols, u);
-        store_chunk(qr, at, cols, u, scale);
+        Chunk<kDT, kWhole> u;
+        u.load(xr, at, cols);
+        store_chunk(qr, at, cols, u, scale, inv);
     }
 }
 
@@ -116,8 +94,12 @@ hipError_t launch(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t
                   float* scale, int32_t* status, hipStream_t stream)
 {
     const int64_t wgs = (rows + kThreads / kLanes - 1) / (kThreads / kLanes);
-    hipLaunchKernelGGL((quantize_rows_kernel<kDT, kLanes, kKeep>), dim3((unsigned)wgs),
-                       dim3(kThreads), 0, stream, x, ldx, rows, cols, q, ldq, scale, status);
+    if (cols % kChunk == 0)
+        hipLaunchKernelGGL((quantize_rows_kernel<kDT, kLanes, kKeep, true>), dim3((unsigned)wgs),
+                           dim3(kThreads), 0, stream, x, ldx, rows, cols, q, ldq, scale, status);
+    else
+        hipLaunchKernelGGL((quantize_rows_kernel<kDT, kLanes, kKeep, false>), dim3((unsigned)wgs),
+                           dim3(kThreads), 0, stream, x, ldx, rows, cols, q, ldq, scale, status);
     return hipGetLastError();
 }
 

@@ -12,8 +12,13 @@ stride of their own (slices of larger tensors are taken as they are).
 from __future__ import annotations
 
 import ctypes
+import sys
 
 import torch
+
+# The package, whose helpers and loaded library the calls below use (it imports
+# this module before it defines them).
+iq = sys.modules[__package__]
 
 # iq_dtype_t of the values these operators take.
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -41,11 +46,6 @@ def declare(L):
                        "iq_expert_sort_workspace": [i64, i32]}.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, i64
-
-
-def _pkg():
-    import ggml_iq_codebook_amd as iq
-    return iq
 
 
 def _matrix(t, name, dtype=None):
@@ -90,8 +90,9 @@ def _same_device(first, *others):
     return index
 
 
-def _stream(index):
-    return torch.cuda.current_stream(index).cuda_stream
+# The current stream's handle, without the Stream object that
+# torch.cuda.current_stream builds around it (1.1 us a call).
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _output(out, rows, cols, dtype, device, name):
@@ -112,7 +113,6 @@ def quantize_rows(x, *, status=None, check=True):
     makes the weight of the products below.  A row with a NaN or an infinity is
     reported (IQ_ERR_NONFINITE) and written as zeros.
     """
-    iq = _pkg()
     ldx = _matrix(x, "x")
     rows, cols = x.shape
     index = _same_device(x, status)
@@ -135,7 +135,6 @@ def int8_matmul(x, x_scale, w, w_scale, *, dtype=torch.bfloat16, out=None):
     ``quantize_rows`` gives them).  The sums are exact.  Returns
     [tokens, channels] in ``dtype`` (or in the type of ``out``).
     """
-    iq = _pkg()
     ldx, ldw = _matrix(x, "x", torch.int8), _matrix(w, "w", torch.int8)
     tokens, depth = x.shape
     channels = w.shape[0]
@@ -162,7 +161,6 @@ def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
     has its type.  A token with a NaN or an infinity is reported
     (IQ_ERR_NONFINITE) and answered with zeros.
     """
-    iq = _pkg()
     ldx, ldw = _matrix(x, "x"), _matrix(w, "w", torch.int8)
     tokens, depth = x.shape
     channels = w.shape[0]
@@ -195,7 +193,6 @@ def int8_expert_matmul(x, x_scale, w, w_scale, offsets, order=None, *, top_k=1,
     ``order`` it is row p of ``x`` (already dispatched).  Rows of dropped
     choices are zeros.
     """
-    iq = _pkg()
     ldx = _matrix(x, "x", torch.int8)
     tokens, depth = x.shape
     if not isinstance(w, torch.Tensor):
@@ -237,7 +234,6 @@ def expert_sort(experts_of, num_experts, *, status=None, check=True):
     expert's first place.  Equal choices keep their order, dropped ones come
     last, from offsets[num_experts] on.
     """
-    iq = _pkg()
     if not isinstance(experts_of, torch.Tensor):
         raise TypeError("experts_of must be a torch.Tensor")
     if not experts_of.is_cuda:
@@ -280,7 +276,6 @@ def _route(position, offsets):
 def expert_dispatch(x, position, offsets, *, out=None):
     """Tokens copied to the places of their choices: [tokens * top_k, width],
     row position[t, j] holding ``x[t]`` (zeros where the choice was dropped)."""
-    iq = _pkg()
     ldx = _matrix(x, "x")
     tokens, top_k, experts = _route(position, offsets)
     if x.shape[0] != tokens:
@@ -305,7 +300,6 @@ def _sorted(t, name, tokens, top_k):
 def expert_dispatch_backward(grad, position, offsets, *, out=None):
     """The gradient of ``expert_dispatch``: for the gradient of its result, that
     of ``x``, the sum over each token's kept choices."""
-    iq = _pkg()
     tokens, top_k, experts = _route(position, offsets)
     ldg = _sorted(grad, "grad", tokens, top_k)
     width = grad.shape[1]
@@ -321,7 +315,6 @@ def expert_dispatch_backward(grad, position, offsets, *, out=None):
 def expert_combine(y, position, offsets, weights, *, out=None):
     """Rows brought back to their tokens: out[t] = the sum over the kept choices
     j of weights[t, j] * y[position[t, j]] (``weights`` fp32 [tokens, top_k])."""
-    iq = _pkg()
     tokens, top_k, experts = _route(position, offsets)
     ldy = _sorted(y, "y", tokens, top_k)
     width = y.shape[1]
@@ -338,7 +331,6 @@ def expert_combine(y, position, offsets, weights, *, out=None):
 def expert_combine_backward(grad, y, position, offsets, weights):
     """The gradients of ``expert_combine`` for the gradient ``grad`` [tokens,
     width] of its result: (that of ``y``, that of ``weights``)."""
-    iq = _pkg()
     tokens, top_k, experts = _route(position, offsets)
     ldy = _sorted(y, "y", tokens, top_k)
     width = y.shape[1]

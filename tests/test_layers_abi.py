@@ -79,13 +79,14 @@ def test_int8_matmul_refusals(lib):
 
 
 def test_int8_linear_refusals(lib):
-    need = lib.iq_int8_linear_workspace(4, 70)
-    assert need == 4 * 80 + 16
+    need = lib.iq_int8_linear_workspace(40, 70)
+    assert need == 40 * 80 + 160
+    assert lib.iq_int8_linear_workspace(4, 70) == 0                      # a few tokens: none
     assert lib.iq_int8_linear_workspace(0, 70) == 0
     assert lib.iq_int8_linear_workspace(4, 0) == 0
     assert lib.iq_int8_linear_workspace(4, 131072) == 0
 
-    def f(dt=1, x=FAKE, ldx=70, w=FAKE, ldw=70, ws=FAKE, t=4, n=8, k=70, y=FAKE, ldy=8, wk=FAKE,
+    def f(dt=1, x=FAKE, ldx=70, w=FAKE, ldw=70, ws=FAKE, t=40, n=8, k=70, y=FAKE, ldy=8, wk=FAKE,
           wb=need, st=FAKE):
         return lib.iq_int8_linear(dt, x, ldx, w, ldw, ws, t, n, k, y, ldy, wk, wb, st, None)
     for name in ("x", "w", "ws", "y", "wk"):
