@@ -188,7 +188,18 @@ __device__ __forceinline__ int64_t place_of(const Route& r, int64_t token, int j
     return p >= 0 && p < r.tokens * r.top_k ? p : -1;
 }
 
-template <int kDT>
+// This thread's token.  Where a row is shared by whole waves the token is the
+// same for all of a wave's lanes, and its places and weights are read as
+// scalars, all at once, ahead of the rows.
+template <bool kWaves>
+__device__ __forceinline__ int64_t token_of(int lanes)
+{
+    const int in_block = threadIdx.x / lanes;
+    return (int64_t)blockIdx.x * (kThreads / lanes) +
+           (kWaves ? __builtin_amdgcn_readfirstlane(in_block) : in_block);
+}
+
+template <int kDT, bool kWaves>
 __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
                                                                    const void* __restrict__ x,
                                                                    int64_t ldx,
@@ -196,7 +207,7 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
                                                                    int64_t lds, int lanes)
 {
     typedef typename Value<kDT>::raw raw;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    const int64_t token = token_of<kWaves>(lanes);
     if (token >= r.tokens) return;
     const int64_t kept = *r.kept;
     const raw* xr = static_cast<const raw*>(x) + token * ldx;
@@ -217,9 +228,41 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
     }
 }
 
+// kGroup choices of a token: their places, weights and which of them count.
+// `row` is a place that is there in any case (0 where the choice's is not), so
+// that rows are loaded without branches between the loads; what the row of a
+// choice that does not count holds is left out of every sum.
+template <int kGroup>
+struct Choices {
+    int64_t place[kGroup];
+    int64_t row[kGroup];
+    float weight[kGroup];
+    bool live[kGroup];
+    __device__ __forceinline__ Choices(const Route& r, int64_t token, int j0, int64_t kept,
+                                       const float* weights)
+    {
+        int32_t p[kGroup];
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const int64_t c = token * r.top_k + min(j0 + g, r.top_k - 1);
+            p[g] = r.position[c];
+            weight[g] = weights ? weights[c] : 1.0f;
+        }
+        const int64_t rows = r.tokens * r.top_k;
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const bool there = (j0 + g < r.top_k) & (p[g] >= 0) & (p[g] < rows);
+            place[g] = there ? p[g] : -1;
+            live[g] = there & (p[g] < kept);
+            row[g] = live[g] ? p[g] : 0;
+        }
+    }
+};
+
 // kWeighted: combine; otherwise the gradient of dispatch.  The rows of kGroup
 // choices are on their way at once; the sum keeps the order of the choices.
-template <int kDT, bool kWeighted>
+// Bound by HBM's reads: a row is read once, without keeping it in the caches.
+template <int kDT, bool kWeighted, int kGroup, bool kWaves>
 __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
                                                                   const void* __restrict__ y,
                                                                   int64_t ldy,
@@ -228,100 +271,127 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
                                                                   int64_t ldo, int lanes)
 {
     typedef typename Value<kDT>::raw raw;
-    constexpr int kGroup = 4;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    constexpr int kN = Row<kDT>::kN;
+    const int64_t token = token_of<kWaves>(lanes);
     if (token >= r.tokens) return;
     const int64_t kept = *r.kept;
     raw* to = static_cast<raw*>(out) + token * ldo;
-    for (int64_t at = (int64_t)(threadIdx.x % lanes) * Row<kDT>::kN; at < r.width;
-         at += (int64_t)lanes * Row<kDT>::kN) {
-        float sum[Row<kDT>::kN] = {};
+    const int64_t first = (int64_t)(threadIdx.x % lanes) * kN, step = (int64_t)lanes * kN;
+    for (int64_t at = first; at < r.width; at += step) {
+        float sum[kN] = {};
         for (int j0 = 0; j0 < r.top_k; j0 += kGroup) {
-            // Rows that do not count are replaced by row 0, which is there, and
-            // left out of the sum: no branch keeps the loads apart.
-            Row<kDT> v[kGroup];
-            float w[kGroup];
-            bool live[kGroup];
-            const raw* from[kGroup];
+            const Choices<kGroup> c(r, token, j0, kept, kWeighted ? weights : nullptr);
+            if (at + kN <= r.width) {
+                Row<kDT> v[kGroup];
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
-                const int j = min(j0 + g, r.top_k - 1);
-                const int64_t p = place_of(r, token, j);
-                live[g] = j0 + g < r.top_k && p >= 0 && p < kept;
-                w[g] = kWeighted ? weights[token * r.top_k + j] : 1.0f;
-                from[g] = static_cast<const raw*>(y) + (live[g] ? p : 0) * ldy;
-            }
-            if (at + Row<kDT>::kN <= r.width) {
+                for (int g = 0; g < kGroup; ++g)
+                    v[g].load_once(static_cast<const raw*>(y) + c.row[g] * ldy + at);
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g) __builtin_memcpy(v[g].u, from[g] + at, 16);
+                for (int g = 0; g < kGroup; ++g)
+                    if (c.live[g]) {
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            sum[i] += kWeighted ? c.weight[g] * v[g][i] : v[g][i];
+                    }
             } else {
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g) v[g].load(from[g], at, r.width);
+                for (int g = 0; g < kGroup; ++g)
+                    if (c.live[g]) {
+                        Row<kDT> v;
+                        v.load(static_cast<const raw*>(y) + c.row[g] * ldy, at, r.width);
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            sum[i] += kWeighted ? c.weight[g] * v[i] : v[i];
+                    }
             }
-#pragma unroll
-            for (int g = 0; g < kGroup; ++g)
-#pragma unroll
-                for (int i = 0; i < Row<kDT>::kN; ++i) {
-                    const float term = kWeighted ? w[g] * v[g][i] : v[g][i];
-                    sum[i] = live[g] ? sum[i] + term : sum[i];
-                }
         }
         Row<kDT> o;
         o.zero();
 #pragma unroll
-        for (int i = 0; i < Row<kDT>::kN; ++i) o.set(i, sum[i]);
+        for (int i = 0; i < kN; ++i) o.set(i, sum[i]);
         o.store(to, at, r.width);
     }
 }
 
-// A workgroup per token: its gradient is scaled into the rows of its choices,
-// and multiplied with what those rows held, choice by choice.
-template <int kDT>
+// A token's gradient is scaled into the rows of its choices, and multiplied
+// with what those rows held, kGroup choices at a time.  kLanes: a wave or the
+// workgroup shares a token.
+template <int kDT, int kLanes>
 __global__ __launch_bounds__(kThreads) void expert_combine_backward_kernel(
     Route r, const void* __restrict__ out_grad, int64_t ldo, const void* __restrict__ y,
     int64_t ldy, const float* __restrict__ weights, void* __restrict__ y_grad, int64_t ldg,
     float* __restrict__ weights_grad)
 {
     typedef typename Value<kDT>::raw raw;
-    __shared__ float parts[kThreads / kWave];
-    const int64_t token = blockIdx.x;
+    constexpr int kGroup = 4, kN = Row<kDT>::kN;
+    __shared__ float parts[kThreads / kWave][kGroup];
+    const int64_t token = token_of<true>(kLanes);
+    // Tokens beyond the last only occur where a token is a wave's: no barrier then.
+    if (token >= r.tokens) return;
+    const int lane = threadIdx.x % kLanes;
     const int64_t kept = *r.kept;
     const raw* gr = static_cast<const raw*>(out_grad) + token * ldo;
-    for (int j = 0; j < r.top_k; ++j) {
-        const int64_t p = place_of(r, token, j);
-        const bool live = p >= 0 && p < kept;
-        const float w = live ? weights[token * r.top_k + j] : 0.0f;
-        float dot = 0.0f;
-        if (p >= 0) {
-            const raw* yr = static_cast<const raw*>(y) + p * ldy;
-            raw* to = static_cast<raw*>(y_grad) + p * ldg;
-            for (int64_t at = (int64_t)threadIdx.x * Row<kDT>::kN; at < r.width;
-                 at += (int64_t)kThreads * Row<kDT>::kN) {
-                Row<kDT> g, v, d;
+    for (int j0 = 0; j0 < r.top_k; j0 += kGroup) {
+        const Choices<kGroup> c(r, token, j0, kept, weights);
+        float dot[kGroup] = {};
+        for (int64_t at = (int64_t)lane * kN; at < r.width; at += (int64_t)kLanes * kN) {
+            // One choice's part, from its row's vector.
+            auto part = [&](int g, const Row<kDT>& grad, const Row<kDT>& v) {
+                Row<kDT> d;
                 d.zero();
-                if (live) {
-                    g.load(gr, at, r.width);
-                    v.load(yr, at, r.width);
+                if (c.live[g]) {
 #pragma unroll
-                    for (int i = 0; i < Row<kDT>::kN; ++i) {
-                        dot += g[i] * v[i];
-                        d.set(i, w * g[i]);
+                    for (int i = 0; i < kN; ++i) {
+                        dot[g] += grad[i] * v[i];
+                        d.set(i, c.weight[g] * grad[i]);
                     }
                 }
-                d.store(to, at, r.width);
+                if (c.place[g] >= 0)
+                    d.store(static_cast<raw*>(y_grad) + c.place[g] * ldg, at, r.width);
+            };
+            Row<kDT> grad;
+            grad.load(gr, at, r.width);
+            if (at + kN <= r.width) {
+                Row<kDT> v[kGroup];
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g)
+                    v[g].load_once(static_cast<const raw*>(y) + c.row[g] * ldy + at);
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) part(g, grad, v[g]);
+            } else {
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    Row<kDT> v;
+                    v.zero();
+                    if (c.live[g])
+                        v.load(static_cast<const raw*>(y) + c.row[g] * ldy, at, r.width);
+                    part(g, grad, v);
+                }
             }
         }
 #pragma unroll
-        for (int d = kWave / 2; d; d >>= 1) dot += __shfl_xor(dot, d);
-        if (threadIdx.x % kWave == 0) parts[threadIdx.x / kWave] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float sum = parts[0];
+        for (int g = 0; g < kGroup; ++g)
 #pragma unroll
-            for (int i = 1; i < kThreads / kWave; ++i) sum += parts[i];
-            weights_grad[token * r.top_k + j] = sum;
+            for (int d = kWave / 2; d; d >>= 1) dot[g] += __shfl_xor(dot[g], d);
+        if (kLanes > kWave) {
+            if (threadIdx.x % kWave == 0) {
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) parts[threadIdx.x / kWave][g] = dot[g];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+                dot[g] = parts[0][g];
+#pragma unroll
+                for (int i = 1; i < kThreads / kWave; ++i) dot[g] += parts[i][g];
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        if (lane == 0) {
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g)
+                if (j0 + g < r.top_k) weights_grad[token * r.top_k + j0 + g] = dot[g];
+        }
     }
 }
 
@@ -383,11 +453,41 @@ hipError_t launch_expert_dispatch(int dtype, const Route& r, const void* x, int6
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
         const int lanes = lanes_for(r.width, Row<kDT>::kN);
-        const int64_t wgs = (r.tokens + kThreads / lanes - 1) / (kThreads / lanes);
-        hipLaunchKernelGGL((expert_dispatch_kernel<kDT>), dim3((unsigned)wgs), dim3(kThreads), 0,
-                           stream, r, x, ldx, sorted, lds, lanes);
+        const dim3 wgs((unsigned)((r.tokens + kThreads / lanes - 1) / (kThreads / lanes)));
+        if (lanes >= kWave)
+            hipLaunchKernelGGL((expert_dispatch_kernel<kDT, true>), wgs, dim3(kThreads), 0, stream,
+                               r, x, ldx, sorted, lds, lanes);
+        else
+            hipLaunchKernelGGL((expert_dispatch_kernel<kDT, false>), wgs, dim3(kThreads), 0,
+                               stream, r, x, ldx, sorted, lds, lanes);
         return hipGetLastError();
     });
+}
+
+template <int kDT, bool kWeighted, int kGroup, bool kWaves>
+static hipError_t combine_as(const Route& r, const void* y, int64_t ldy, const float* weights,
+                             void* out, int64_t ldo, int lanes, hipStream_t stream)
+{
+    const dim3 wgs((unsigned)((r.tokens + kThreads / lanes - 1) / (kThreads / lanes)));
+    hipLaunchKernelGGL((expert_combine_kernel<kDT, kWeighted, kGroup, kWaves>), wgs,
+                       dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
+    return hipGetLastError();
+}
+
+// As many rows at once as there are choices, 2, 4 or 8; 4 where lanes of a wave
+// work on different tokens.
+template <int kDT, bool kWeighted>
+static hipError_t combine_with(const Route& r, const void* y, int64_t ldy, const float* weights,
+                               void* out, int64_t ldo, hipStream_t stream)
+{
+    const int lanes = lanes_for(r.width, Row<kDT>::kN);
+    if (lanes < kWave)
+        return combine_as<kDT, kWeighted, 4, false>(r, y, ldy, weights, out, ldo, lanes, stream);
+    if (r.top_k <= 2)
+        return combine_as<kDT, kWeighted, 2, true>(r, y, ldy, weights, out, ldo, lanes, stream);
+    if (r.top_k <= 4)
+        return combine_as<kDT, kWeighted, 4, true>(r, y, ldy, weights, out, ldo, lanes, stream);
+    return combine_as<kDT, kWeighted, 8, true>(r, y, ldy, weights, out, ldo, lanes, stream);
 }
 
 hipError_t launch_expert_combine(int dtype, const Route& r, const void* y, int64_t ldy,
@@ -395,15 +495,8 @@ hipError_t launch_expert_combine(int dtype, const Route& r, const void* y, int64
 {
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
-        const int lanes = lanes_for(r.width, Row<kDT>::kN);
-        const int64_t wgs = (r.tokens + kThreads / lanes - 1) / (kThreads / lanes);
-        if (weights)
-            hipLaunchKernelGGL((expert_combine_kernel<kDT, true>), dim3((unsigned)wgs),
-                               dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
-        else
-            hipLaunchKernelGGL((expert_combine_kernel<kDT, false>), dim3((unsigned)wgs),
-                               dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
-        return hipGetLastError();
+        return weights ? combine_with<kDT, true>(r, y, ldy, weights, out, ldo, stream)
+                       : combine_with<kDT, false>(r, y, ldy, weights, out, ldo, stream);
     });
 }
 
@@ -414,9 +507,17 @@ hipError_t launch_expert_combine_backward(int dtype, const Route& r, const void*
 {
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
-        hipLaunchKernelGGL((expert_combine_backward_kernel<kDT>), dim3((unsigned)r.tokens),
-                           dim3(kThreads), 0, stream, r, out_grad, ldo, y, ldy, weights, y_grad,
-                           ldg, weights_grad);
+        // Two vectors a lane of a wave at most, else the workgroup.
+        if (r.width <= 2 * kWave * Row<kDT>::kN) {
+            const dim3 wgs((unsigned)((r.tokens + kThreads / kWave - 1) / (kThreads / kWave)));
+            hipLaunchKernelGGL((expert_combine_backward_kernel<kDT, kWave>), wgs, dim3(kThreads),
+                               0, stream, r, out_grad, ldo, y, ldy, weights, y_grad, ldg,
+                               weights_grad);
+        } else {
+            hipLaunchKernelGGL((expert_combine_backward_kernel<kDT, kThreads>),
+                               dim3((unsigned)r.tokens), dim3(kThreads), 0, stream, r, out_grad,
+                               ldo, y, ldy, weights, y_grad, ldg, weights_grad);
+        }
         return hipGetLastError();
     });
 }

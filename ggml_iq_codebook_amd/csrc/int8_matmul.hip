@@ -131,33 +131,26 @@ __device__ __forceinline__ int64_t token_of(const Int8Product& p, int64_t r)
 // Writing results
 // ---------------------------------------------------------------------------
 
-// Four consecutive channels of one row of y.
-__device__ __forceinline__ void store4(const Int8Product& p, int64_t row, int channel,
-                                       const float (&f)[4])
+// kN consecutive channels of one row of y, in its type.
+template <int kDT, int kN>
+__device__ __forceinline__ void store_channels(const Int8Product& p, int64_t row, int channel,
+                                               const float (&f)[kN])
 {
-    const int64_t at = row * p.ldy + channel;
-    if (p.out_dtype == IQ_DTYPE_F32) {
-        float* to = static_cast<float*>(p.y) + at;
-        if (channel + 4 <= p.channels)
-            __builtin_memcpy(to, f, 16);
-        else
-            for (int i = 0; i < 4; ++i)
-                if (channel + i < p.channels) to[i] = f[i];
-        return;
-    }
-    uint16_t h[4];
+    typedef typename Value<kDT>::raw raw;
+    raw* to = static_cast<raw*>(p.y) + row * p.ldy + channel;
+    raw v[kN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = p.out_dtype == IQ_DTYPE_BF16 ? Value<IQ_DTYPE_BF16>::store(f[i])
-                                            : Value<IQ_DTYPE_F16>::store(f[i]);
-    uint16_t* to = static_cast<uint16_t*>(p.y) + at;
-    if (channel + 4 <= p.channels)
-        __builtin_memcpy(to, h, 8);
-    else
-        for (int i = 0; i < 4; ++i)
-            if (channel + i < p.channels) to[i] = h[i];
+    for (int i = 0; i < kN; ++i) v[i] = Value<kDT>::store(f[i]);
+    if (channel + kN <= p.channels) {
+        __builtin_memcpy(to, v, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (channel + i < p.channels) to[i] = v[i];
+    }
 }
 
+// The dropped rows of a tile: zeros are zeros in every type.
 template <int kRows, int kChannels, int kThreads>
 __device__ __forceinline__ void store_zeros(const Int8Product& p, const Tile& t)
 {
@@ -165,15 +158,17 @@ __device__ __forceinline__ void store_zeros(const Int8Product& p, const Tile& t)
     for (int i = threadIdx.x; i < kRows * (kChannels / 4); i += kThreads) {
         const int64_t row = t.row0 + i / (kChannels / 4);
         const int channel = t.channel_tile * kChannels + i % (kChannels / 4) * 4;
-        if (row < t.row_end && channel < p.channels) store4(p, row, channel, zero);
+        if (row >= t.row_end || channel >= p.channels) continue;
+        if (p.out_dtype == IQ_DTYPE_F32)
+            store_channels<IQ_DTYPE_F32>(p, row, channel, zero);
+        else
+            store_channels<IQ_DTYPE_F16>(p, row, channel, zero);
     }
 }
 
 // ---------------------------------------------------------------------------
 // The tile kernel
 // ---------------------------------------------------------------------------
-
-__device__ const uint4 zeros[1] = {{0u, 0u, 0u, 0u}};
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void global_void;
@@ -184,18 +179,30 @@ __device__ __forceinline__ void copy_to_lds(const int8_t* from, int8_t* to)
     __builtin_amdgcn_global_load_lds((global_void*)(uintptr_t)from, (lds_void*)to, 16, 0, 0);
 }
 
+// 16 bytes at any alignment.
+__device__ __forceinline__ uint4 load16(const int8_t* from)
+{
+    uint4 v;
+    __builtin_memcpy(&v, from, 16);
+    return v;
+}
+
 // 16 bytes of a row from depth `at`, zeros beyond its end, at any alignment.
 __device__ __forceinline__ uint4 load_codes(const int8_t* row, int at, int depth)
 {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (at + 16 <= depth) {
-        __builtin_memcpy(&v, row + at, 16);
+        v = load16(row + at);
     } else if (at < depth) {
-        uint32_t u[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (at + i < depth) u[i / 4] |= (uint32_t)(uint8_t)row[at + i] << (8 * (i % 4));
-        v = make_uint4(u[0], u[1], u[2], u[3]);
+        uint64_t u[2] = {0u, 0u};
+#pragma unroll 1
+        for (int i = 0; i < depth - at; ++i) {
+            const uint64_t byte = (uint64_t)(uint8_t)row[at + i] << (8 * (i % 8));
+            u[0] |= i < 8 ? byte : 0u;
+            u[1] |= i < 8 ? 0u : byte;
+        }
+        v = make_uint4((uint32_t)u[0], (uint32_t)(u[0] >> 32), (uint32_t)u[1],
+                       (uint32_t)(u[1] >> 32));
     }
     return v;
 }
@@ -206,7 +213,7 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* row, int at, int depth
 template <int kDepth>
 __device__ __forceinline__ int swizzle(int row)
 {
-    return kDepth == 64 ? (row >> 1) & 3 : (kDepth == 128 ? row & 7 : row & 15);
+    return kDepth == 64 ? (row >> 1) & 3 : row & 7;
 }
 
 // Waits until at most kLeft of this wave's loads are under way and all its LDS
@@ -219,15 +226,20 @@ __device__ __forceinline__ void wait_and_meet()
 
 // kWT x kWC waves share a tile of kRows rows of y by kChannels channels, each
 // a part of kRows/kWT by kChannels/kWC, in steps of kDepth of the depth.  The
-// tiles of both operands go through a ring of kStages buffers in LDS.
+// tiles of both operands go through a ring of buffers in LDS; what the depth
+// leaves beyond whole steps has a buffer of its own, filled at the start.
 //
 // kDirect: rows start on 16 bytes, and pieces are copied straight into LDS,
-// kStages - 1 steps ahead.  Otherwise they pass through registers, kAhead
-// steps ahead, with the ends of rows cut byte by byte, into two buffers.
+// kStages - 1 steps ahead.  Otherwise they pass through registers, two steps
+// ahead, into two buffers.
 //
 // kPingPong (8 waves, two on a SIMD): the second four waves run half a step
 // behind, so on each SIMD one wave multiplies while the other reads its
 // operands; a step is two barriers long.
+//
+// Results go through LDS too where a wave has 32 channels or more: written as
+// the matrix instructions leave them, 4 channels a lane, and read back as
+// whole rows of its channels, 16 bytes a lane, so that stores fill cache lines.
 template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,
           bool kDirect, bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kernel(Int8Product p,
@@ -239,9 +251,9 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
     constexpr int kRowsPerLoad = kWave / kPieces;
     constexpr int kLoads = (kRows + kChannels) / kRowsPerLoad / kWaves;   // a wave's
     constexpr int kBuffers = kDirect ? kStages : 2;
-    constexpr int kAhead = 2;
     static_assert(kLoads * kRowsPerLoad * kWaves == kRows + kChannels && kFT > 0 && kFC > 0, "tile");
-    __shared__ __align__(1024) int8_t staged[kBuffers][(kRows + kChannels) * kDepth];
+    constexpr int kBytes = (kRows + kChannels) * kDepth;
+    __shared__ __align__(1024) int8_t staged[kBuffers + 1][kBytes];
 
     const Tile t = kExperts ? expert_tile<kRows>(p, channel_tiles)
                             : dense_tile<kRows>(p, channel_tiles);
@@ -258,39 +270,47 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
     // Staged rows: the weight's channels, then the tokens.  Rows beyond the
     // last repeat it: their results are not stored.
     const int8_t* from[kLoads];
-    int piece[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int r = (wave * kLoads + i) * kRowsPerLoad + lane / kPieces;
-        piece[i] = ((lane % kPieces) ^ swizzle<kDepth>(r)) * 16;
+        const int at = ((lane % kPieces) ^ swizzle<kDepth>(r)) * 16;
         if (r < kChannels) {
-            from[i] = w + (int64_t)min(channel0 + r, p.channels - 1) * p.ldw;
+            from[i] = w + (int64_t)min(channel0 + r, p.channels - 1) * p.ldw + at;
         } else {
             const int64_t row = min(t.row0 + r - kChannels, t.row_end - 1);
-            from[i] = p.x + (kExperts ? token_of(p, row) : row) * p.ldx;
+            from[i] = p.x + (kExperts ? token_of(p, row) : row) * p.ldx + at;
         }
     }
-    const int steps = (p.depth + kDepth - 1) / kDepth;
-    // Steps before this one lie within the rows.
-    const int whole = p.depth / kDepth;
+    const int steps = p.depth / kDepth;
+    const int rest = p.depth - steps * kDepth;
+    // The rest of the depth: through registers, its end cut byte by byte.
+    auto stage_rest = [&]() {
+        if (rest == 0) return;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (wave * kLoads + i) * kRowsPerLoad + lane / kPieces;
+            const int at = ((lane % kPieces) ^ swizzle<kDepth>(r)) * 16;
+            *reinterpret_cast<uint4*>(&staged[kBuffers][(wave * kLoads + i) * 1024 + lane * 16]) =
+                load_codes(from[i] + (int64_t)steps * kDepth - at, at, rest);
+        }
+    };
 
     v4i acc[kFC][kFT] = {};
     const int wt = wave % kWT, wc = wave / kWT;
+    const int quarter = lane / 16;
     const int row_c = wc * kFC * 16 + lane % 16;
     const int row_t = kChannels + wt * kFT * 16 + lane % 16;
-    const int quarter = lane / 16;
     constexpr int kParts = kDepth / 64;
     auto read = [&](int b, int k, v4i (&a)[kFC], v4i (&x)[kFT]) {
+        const int piece = 4 * k + quarter;
 #pragma unroll
         for (int i = 0; i < kFC; ++i)
             a[i] = *reinterpret_cast<const v4i*>(
-                &staged[b][(row_c + i * 16) * kDepth +
-                           ((4 * k + quarter) ^ swizzle<kDepth>(row_c)) * 16]);
+                &staged[b][(row_c + i * 16) * kDepth + (piece ^ swizzle<kDepth>(row_c)) * 16]);
 #pragma unroll
         for (int j = 0; j < kFT; ++j)
             x[j] = *reinterpret_cast<const v4i*>(
-                &staged[b][(row_t + j * 16) * kDepth +
-                           ((4 * k + quarter) ^ swizzle<kDepth>(row_t)) * 16]);
+                &staged[b][(row_t + j * 16) * kDepth + (piece ^ swizzle<kDepth>(row_t)) * 16]);
     };
     auto multiply = [&](const v4i (&a)[kFC], const v4i (&x)[kFT]) {
 #pragma unroll
@@ -302,40 +322,17 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
 
     if constexpr (kDirect) {
         auto fetch = [&](int b, int step) {
-            if (step < whole) {
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    copy_to_lds(from[i] + (int64_t)step * kDepth + piece[i],
-                                &staged[b][(wave * kLoads + i) * 1024]);
-            } else {
-                // The end of the rows: pieces beyond it are zeros, and the piece
-                // that holds it is cut in registers.
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int at = step * kDepth + piece[i];
-                    copy_to_lds(at + 16 <= p.depth ? from[i] + at
-                                                   : reinterpret_cast<const int8_t*>(zeros),
-                                &staged[b][(wave * kLoads + i) * 1024]);
-                }
-                if (p.depth % 16) {
-                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        const int at = step * kDepth + piece[i];
-                        if (at < p.depth && at + 16 > p.depth)
-                            *reinterpret_cast<uint4*>(
-                                &staged[b][(wave * kLoads + i) * 1024 + lane * 16]) =
-                                load_codes(from[i], at, p.depth);
-                    }
-                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                }
-            }
+            for (int i = 0; i < kLoads; ++i)
+                copy_to_lds(from[i] + (int64_t)step * kDepth,
+                            &staged[b][(wave * kLoads + i) * 1024]);
         };
         constexpr int kLeft = (kStages - 2) * kLoads;
         static_assert(kLeft < 64, "vmcnt holds 6 bits");
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i)
             if (i < steps) fetch(i, i);
+        stage_rest();
         if constexpr (kPingPong) {
             const bool late = wave >= kWaves / 2;
             if (steps >= kStages - 1)
@@ -351,8 +348,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
                     v4i a[kParts][kFC], x[kParts][kFT];
 #pragma unroll
                     for (int k = 0; k < kParts; ++k) read(u, k, a[k], x[k]);
-                    // The buffer of step s - 1: both halves read it before the
-                    // last barrier.  Step s + 1 has to be there for the next.
+                    // Into the buffer of step s - 1, which both halves read before
+                    // the last barrier.  Step s + 1 has to be there for the next.
                     if (s + kStages - 1 < steps) {
                         fetch((u + kStages - 1) % kStages, s + kStages - 1);
                         wait_and_meet<kLeft>();
@@ -391,14 +388,18 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
             }
         }
     } else {
-        uint4 passing[kAhead][kLoads];
+        uint4 passing[2][kLoads];
         auto fetch = [&](int set, int step) {
+            // Beyond the last step the last one again: not used.
+            const int64_t at = (int64_t)min(step, max(steps - 1, 0)) * kDepth;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                passing[set][i] = load_codes(from[i], step * kDepth + piece[i], p.depth);
+            for (int i = 0; i < kLoads; ++i) passing[set][i] = load16(from[i] + at);
         };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(i, i);
+        if (steps > 0) {
+            fetch(0, 0);
+            fetch(1, 1);
+        }
+        stage_rest();
         for (int s0 = 0; s0 < steps; s0 += 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
                     *reinterpret_cast<uint4*>(&staged[u][(wave * kLoads + i) * 1024 + lane * 16]) =
                         passing[u][i];
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                fetch(u, s + kAhead);
+                fetch(u, s + 2);
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) {
                     v4i a[kFC], x[kFT];
@@ -420,24 +421,89 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
             }
         }
     }
-
+    if (rest) {
+        wait_and_meet<0>();
 #pragma unroll
-    for (int j = 0; j < kFT; ++j) {
-        const int64_t row = t.row0 + (wt * kFT + j) * 16 + lane % 16;
-        if (row >= t.row_end) continue;
-        const float sx = p.x_scale[kExperts ? token_of(p, row) : row];
-        const float* sw = p.w_scale + (int64_t)t.expert * p.channels;
-#pragma unroll
-        for (int i = 0; i < kFC; ++i) {
-            const int channel = channel0 + (wc * kFC + i) * 16 + 4 * quarter;
-            if (channel >= p.channels) continue;
-            float f[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                f[v] = (float)acc[i][j][v] * sx * sw[min(channel + v, p.channels - 1)];
-            store4(p, row, channel, f);
+        for (int k = 0; k < kParts; ++k) {
+            v4i a[kFC], x[kFT];
+            read(kBuffers, k, a, x);
+            multiply(a, x);
         }
     }
+
+    const int wave_channel = channel0 + wc * kFC * 16;
+    const float* sw = p.w_scale + (int64_t)t.expert * p.channels;
+    float scale[kFC][4];
+#pragma unroll
+    for (int i = 0; i < kFC; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            scale[i][v] = sw[min(wave_channel + i * 16 + 4 * quarter + v, p.channels - 1)];
+    // Every wave is done with the staged tiles.
+    if (kFC > 1) wait_and_meet<0>();
+    auto write = [&](auto dt) {
+        constexpr int kDT = decltype(dt)::value;
+        typedef typename Value<kDT>::raw raw;
+        constexpr int kN = 16 / (int)sizeof(raw);
+        // A row of the wave's channels, and some more so that rows start on
+        // different banks.
+        constexpr int kRow = kFC * 16 + kN;
+        constexpr int kLanes = kFC * 16 / kN;             // lanes to a row
+        static_assert(kFC == 1 || kWaves * 16 * kRow * (int)sizeof(raw) <= (kBuffers + 1) * kBytes,
+                      "results fit the staged tiles");
+        raw* mine = reinterpret_cast<raw*>(&staged[0][0]) + wave * 16 * kRow;
+#pragma unroll
+        for (int j = 0; j < kFT; ++j) {
+            const int64_t row0 = t.row0 + (wt * kFT + j) * 16;
+            const int64_t row = min(row0 + lane % 16, t.row_end - 1);
+            const float sx = p.x_scale[kExperts ? token_of(p, row) : row];
+#pragma unroll
+            for (int i = 0; i < kFC; ++i) {
+                float f[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) f[v] = (float)acc[i][j][v] * sx * scale[i][v];
+                if constexpr (kFC == 1) {
+                    const int channel = wave_channel + 4 * quarter;
+                    if (row0 + lane % 16 < t.row_end && channel < p.channels)
+                        store_channels<kDT>(p, row, channel, f);
+                } else {
+                    raw o[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) o[v] = Value<kDT>::store(f[v]);
+                    __builtin_memcpy(__builtin_assume_aligned(
+                                         mine + lane % 16 * kRow + i * 16 + 4 * quarter, 4 * sizeof(raw)),
+                                     o, sizeof(o));
+                }
+            }
+            if constexpr (kFC > 1) {
+                // A wave's own LDS accesses are done in order.
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int s = 0; s < 16 * kLanes / kWave; ++s) {
+                    const int r = (s * kWave + lane) / kLanes, c = (s * kWave + lane) % kLanes * kN;
+                    raw o[kN];
+                    __builtin_memcpy(o, __builtin_assume_aligned(mine + r * kRow + c, 16), 16);
+                    const int channel = wave_channel + c;
+                    if (row0 + r >= t.row_end || channel >= p.channels) continue;
+                    raw* to = static_cast<raw*>(p.y) + (row0 + r) * p.ldy + channel;
+                    if (channel + kN <= p.channels) {
+                        __builtin_memcpy(to, o, 16);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < kN; ++v)
+                            if (channel + v < p.channels) to[v] = o[v];
+                    }
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    };
+    if (p.out_dtype == IQ_DTYPE_BF16)
+        write(Int<IQ_DTYPE_BF16>());
+    else if (p.out_dtype == IQ_DTYPE_F16)
+        write(Int<IQ_DTYPE_F16>());
+    else
+        write(Int<IQ_DTYPE_F32>());
 }
 
 template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,

@@ -65,6 +65,13 @@ struct Row {
                 if (at + i < width) put(i, row[at + i]);
         }
     }
+    // A whole vector that is not read again soon.
+    __device__ __forceinline__ void load_once(const raw* from)
+    {
+        typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+        const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4*>(from));
+        u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+    }
     __device__ __forceinline__ void store(raw* row, int64_t at, int64_t width) const
     {
         if (at + kN <= width) {

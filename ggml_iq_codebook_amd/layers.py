@@ -22,6 +22,8 @@ iq = sys.modules[__package__]
 
 # iq_dtype_t of the values these operators take.
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_CHOICE_BYTES = {torch.int32: 4, torch.int64: 8}
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
 
 
 def declare(L):
@@ -48,12 +50,31 @@ def declare(L):
         f.argtypes, f.restype = args, i64
 
 
-def _matrix(t, name, dtype=None):
-    """A two-dimensional GPU tensor with consecutive values in a row; its row stride."""
+def _on_gpu(t, name):
+    """The index of a tensor's GPU, which has to be the current device: that is
+    where the kernels are launched."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("%s must be on the GPU" % name)
+    if index != torch._C._cuda_getDevice():
+        raise ValueError("%s is on cuda:%d, which is not the current device" % (name, index))
+    return index
+
+
+def _refuse(t, name, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
+    raise ValueError("%s must be on cuda:%d" % (name, index))
+
+
+def _matrix(t, name, index, dtype=None):
+    """A two-dimensional tensor on that GPU with consecutive values in a row; its row stride."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _refuse(t, name, index)
     if dtype is None:
         if t.dtype not in _DTYPES:
             raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
@@ -67,27 +88,15 @@ def _matrix(t, name, dtype=None):
     return stride
 
 
-def _vector(t, dtype, shape, name):
-    """A contiguous GPU tensor of the given shape."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be on the GPU" % name)
+def _vector(t, dtype, shape, name, index):
+    """The address of a contiguous tensor of the given shape on that GPU."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _refuse(t, name, index)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
-
-
-def _same_device(first, *others):
-    """Kernels are launched on the current device, which has to hold every tensor."""
-    index = first.device.index
-    for t in others:
-        if t is not None and t.device.index != index:
-            raise ValueError("all tensors must be on one GPU")
-    if index != torch.cuda.current_device():
-        raise ValueError("the tensors are on cuda:%d, which is not the current device" % index)
-    return index
+    return t.data_ptr()
 
 
 # The current stream's handle, without the Stream object that
@@ -95,13 +104,24 @@ def _same_device(first, *others):
 _stream = torch._C._cuda_getCurrentRawStream
 
 
-def _output(out, rows, cols, dtype, device, name):
+def _output(out, rows, cols, dtype, index, name):
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    stride = _matrix(out, name, dtype)
+        return torch.empty((rows, cols), dtype=dtype, device=_DEVICES[index]), cols
+    stride = _matrix(out, name, index, dtype)
     if out.shape != (rows, cols):
         raise ValueError("%s must be [%d, %d]" % (name, rows, cols))
     return out, stride
+
+
+def _status(status, check, index):
+    """The address of the status word to pass (None: the library waits and
+    returns the data error), and the tensor behind it."""
+    if status is None:
+        if check:
+            return None, None
+        status = torch.zeros(1, dtype=torch.int32, device=_DEVICES[index])
+        return status.data_ptr(), status
+    return _vector(status, torch.int32, status.shape, "status", index), status
 
 
 def quantize_rows(x, *, status=None, check=True):
@@ -113,15 +133,16 @@ def quantize_rows(x, *, status=None, check=True):
     makes the weight of the products below.  A row with a NaN or an infinity is
     reported (IQ_ERR_NONFINITE) and written as zeros.
     """
-    ldx = _matrix(x, "x")
+    index = _on_gpu(x, "x")
+    ldx = _matrix(x, "x", index)
     rows, cols = x.shape
-    index = _same_device(x, status)
-    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    status = iq._status_arg(status, check, x.device)
+    word, status = _status(status, check, index)
+    device = _DEVICES[index]
+    q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    scale = torch.empty((rows,), dtype=torch.float32, device=device)
     code = iq.load().iq_quantize_rows(
         _DTYPES[x.dtype], x.data_ptr(), ldx, rows, cols, q.data_ptr(), cols, scale.data_ptr(),
-        None if status is None else status.data_ptr(), _stream(index))
+        word, _stream(index))
     iq._check(code, "iq_quantize_rows")
     iq._raise_on_status(status, check, "iq_quantize_rows")
     return q, scale
@@ -135,21 +156,22 @@ def int8_matmul(x, x_scale, w, w_scale, *, dtype=torch.bfloat16, out=None):
     ``quantize_rows`` gives them).  The sums are exact.  Returns
     [tokens, channels] in ``dtype`` (or in the type of ``out``).
     """
-    ldx, ldw = _matrix(x, "x", torch.int8), _matrix(w, "w", torch.int8)
+    index = _on_gpu(x, "x")
+    ldx, ldw = _matrix(x, "x", index, torch.int8), _matrix(w, "w", index, torch.int8)
     tokens, depth = x.shape
-    channels = w.shape[0]
-    if w.shape[1] != depth:
+    channels, w_depth = w.shape
+    if w_depth != depth:
         raise ValueError("w must be [channels, %d]" % depth)
-    _vector(x_scale, torch.float32, (tokens,), "x_scale")
-    _vector(w_scale, torch.float32, (channels,), "w_scale")
-    dtype = dtype if out is None else out.dtype
+    xs = _vector(x_scale, torch.float32, (tokens,), "x_scale", index)
+    ws = _vector(w_scale, torch.float32, (channels,), "w_scale", index)
+    if out is not None:
+        dtype = out.dtype
     if dtype not in _DTYPES:
         raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % (dtype,))
-    index = _same_device(x, x_scale, w, w_scale, out)
-    y, ldy = _output(out, tokens, channels, dtype, x.device, "out")
+    y, ldy = _output(out, tokens, channels, dtype, index, "out")
     code = iq.load().iq_int8_matmul(
-        x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), tokens,
-        channels, depth, _DTYPES[dtype], y.data_ptr(), ldy, _stream(index))
+        x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ws, tokens, channels, depth, _DTYPES[dtype],
+        y.data_ptr(), ldy, _stream(index))
     iq._check(code, "iq_int8_matmul")
     return y
 
@@ -161,22 +183,24 @@ def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
     has its type.  A token with a NaN or an infinity is reported
     (IQ_ERR_NONFINITE) and answered with zeros.
     """
-    ldx, ldw = _matrix(x, "x"), _matrix(w, "w", torch.int8)
+    index = _on_gpu(x, "x")
+    ldx, ldw = _matrix(x, "x", index), _matrix(w, "w", index, torch.int8)
     tokens, depth = x.shape
-    channels = w.shape[0]
-    if w.shape[1] != depth:
+    channels, w_depth = w.shape
+    if w_depth != depth:
         raise ValueError("w must be [channels, %d]" % depth)
-    _vector(w_scale, torch.float32, (channels,), "w_scale")
-    index = _same_device(x, w, w_scale, out, status)
-    y, ldy = _output(out, tokens, channels, x.dtype, x.device, "out")
+    ws = _vector(w_scale, torch.float32, (channels,), "w_scale", index)
+    dtype = x.dtype
+    y, ldy = _output(out, tokens, channels, dtype, index, "out")
+    word, status = _status(status, check, index)
     L = iq.load()
-    need = L.iq_int8_linear_workspace(tokens, depth)
-    work = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
-    status = iq._status_arg(status, check, x.device)
+    need, work, space = L.iq_int8_linear_workspace(tokens, depth), None, None
+    if need:
+        work = torch.empty((need,), dtype=torch.uint8, device=_DEVICES[index])
+        space = work.data_ptr()
     code = L.iq_int8_linear(
-        _DTYPES[x.dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, w_scale.data_ptr(), tokens,
-        channels, depth, y.data_ptr(), ldy, None if work is None else work.data_ptr(), need,
-        None if status is None else status.data_ptr(), _stream(index))
+        _DTYPES[dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, ws, tokens, channels, depth,
+        y.data_ptr(), ldy, space, need, word, _stream(index))
     iq._check(code, "iq_int8_linear")
     iq._raise_on_status(status, check, "iq_int8_linear")
     return y
@@ -193,33 +217,32 @@ def int8_expert_matmul(x, x_scale, w, w_scale, offsets, order=None, *, top_k=1,
     ``order`` it is row p of ``x`` (already dispatched).  Rows of dropped
     choices are zeros.
     """
-    ldx = _matrix(x, "x", torch.int8)
+    index = _on_gpu(x, "x")
+    ldx = _matrix(x, "x", index, torch.int8)
     tokens, depth = x.shape
-    if not isinstance(w, torch.Tensor):
-        raise TypeError("w must be a torch.Tensor")
-    if not w.is_cuda:
-        raise ValueError("w must be on the GPU")
+    if not isinstance(w, torch.Tensor) or w.get_device() != index:
+        _refuse(w, "w", index)
     if w.dtype != torch.int8:
         raise TypeError("w must be torch.int8, got %s" % (w.dtype,))
     if w.dim() != 3 or w.shape[2] != depth or (w.stride(2) != 1 and depth != 1):
         raise ValueError("w must be [experts, channels, %d] with consecutive values in a row" % depth)
     experts, channels, _ = w.shape
-    _vector(x_scale, torch.float32, (tokens,), "x_scale")
-    _vector(w_scale, torch.float32, (experts, channels), "w_scale")
-    _vector(offsets, torch.int32, (experts + 1,), "offsets")
-    rows = tokens
+    w_stride, ldw, _ = w.stride()
+    xs = _vector(x_scale, torch.float32, (tokens,), "x_scale", index)
+    ws = _vector(w_scale, torch.float32, (experts, channels), "w_scale", index)
+    ends = _vector(offsets, torch.int32, (experts + 1,), "offsets", index)
+    rows, places = tokens, None
     if order is not None:
-        _vector(order, torch.int32, (tokens * top_k,), "order")
         rows = tokens * top_k
-    dtype = dtype if out is None else out.dtype
+        places = _vector(order, torch.int32, (rows,), "order", index)
+    if out is not None:
+        dtype = out.dtype
     if dtype not in _DTYPES:
         raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % (dtype,))
-    index = _same_device(x, x_scale, w, w_scale, offsets, order, out)
-    y, ldy = _output(out, rows, channels, dtype, x.device, "out")
+    y, ldy = _output(out, rows, channels, dtype, index, "out")
     code = iq.load().iq_int8_expert_matmul(
-        x.data_ptr(), ldx, x_scale.data_ptr(), tokens, None if order is None else order.data_ptr(),
-        top_k, offsets.data_ptr(), experts, rows, w.data_ptr(), w.stride(1), w.stride(0),
-        w_scale.data_ptr(), channels, depth, _DTYPES[dtype], y.data_ptr(), ldy, _stream(index))
+        x.data_ptr(), ldx, xs, tokens, places, top_k, ends, experts, rows, w.data_ptr(), ldw,
+        w_stride, ws, channels, depth, _DTYPES[dtype], y.data_ptr(), ldy, _stream(index))
     iq._check(code, "iq_int8_expert_matmul")
     return y
 
@@ -234,80 +257,76 @@ def expert_sort(experts_of, num_experts, *, status=None, check=True):
     expert's first place.  Equal choices keep their order, dropped ones come
     last, from offsets[num_experts] on.
     """
-    if not isinstance(experts_of, torch.Tensor):
-        raise TypeError("experts_of must be a torch.Tensor")
-    if not experts_of.is_cuda:
-        raise ValueError("experts_of must be on the GPU")
-    if experts_of.dtype not in (torch.int32, torch.int64):
+    index = _on_gpu(experts_of, "experts_of")
+    if experts_of.dtype not in _CHOICE_BYTES:
         raise TypeError("experts_of must be int32 or int64, got %s" % (experts_of.dtype,))
     if experts_of.dim() != 2 or not experts_of.is_contiguous():
         raise ValueError("experts_of must be a contiguous [tokens, top_k] tensor")
     tokens, top_k = experts_of.shape
-    n, device = tokens * top_k, experts_of.device
-    index = _same_device(experts_of, status)
+    n, device = tokens * top_k, _DEVICES[index]
     order = torch.empty((n,), dtype=torch.int32, device=device)
     position = torch.empty((tokens, top_k), dtype=torch.int32, device=device)
     offsets = torch.empty((max(num_experts, 0) + 1,), dtype=torch.int32, device=device)
+    word, status = _status(status, check, index)
     L = iq.load()
-    need = L.iq_expert_sort_workspace(n, num_experts)
-    work = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
-    status = iq._status_arg(status, check, device)
+    need, work, space = L.iq_expert_sort_workspace(n, num_experts), None, None
+    if need:
+        work = torch.empty((need,), dtype=torch.uint8, device=device)
+        space = work.data_ptr()
     code = L.iq_expert_sort(
-        experts_of.data_ptr(), experts_of.element_size(), tokens, top_k, num_experts,
-        order.data_ptr(), position.data_ptr(), offsets.data_ptr(),
-        None if work is None else work.data_ptr(), need,
-        None if status is None else status.data_ptr(), _stream(index))
+        experts_of.data_ptr(), _CHOICE_BYTES[experts_of.dtype], tokens, top_k, num_experts,
+        order.data_ptr(), position.data_ptr(), offsets.data_ptr(), space, need, word,
+        _stream(index))
     iq._check(code, "iq_expert_sort")
     iq._raise_on_status(status, check, "iq_expert_sort")
     return order, position, offsets
 
 
-def _route(position, offsets):
-    """Checks of expert_sort's answers; returns (tokens, top_k, experts)."""
+def _route(position, offsets, index):
+    """Checks of expert_sort's answers: (tokens, top_k, experts, their addresses)."""
     if not isinstance(position, torch.Tensor) or position.dim() != 2:
         raise ValueError("position must be [tokens, top_k]")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must be [num_experts + 1]")
-    _vector(position, torch.int32, position.shape, "position")
-    _vector(offsets, torch.int32, offsets.shape, "offsets")
-    return position.shape[0], position.shape[1], offsets.shape[0] - 1
+    tokens, top_k = position.shape
+    return (tokens, top_k, offsets.shape[0] - 1,
+            _vector(position, torch.int32, position.shape, "position", index),
+            _vector(offsets, torch.int32, offsets.shape, "offsets", index))
+
+
+def _sorted(t, name, rows, index):
+    ld = _matrix(t, name, index)
+    if t.shape[0] != rows:
+        raise ValueError("%s must have %d rows" % (name, rows))
+    return ld
 
 
 def expert_dispatch(x, position, offsets, *, out=None):
     """Tokens copied to the places of their choices: [tokens * top_k, width],
     row position[t, j] holding ``x[t]`` (zeros where the choice was dropped)."""
-    ldx = _matrix(x, "x")
-    tokens, top_k, experts = _route(position, offsets)
-    if x.shape[0] != tokens:
-        raise ValueError("x must have %d rows" % tokens)
-    width = x.shape[1]
-    index = _same_device(x, position, offsets, out)
-    out, ldo = _output(out, tokens * top_k, width, x.dtype, x.device, "out")
+    index = _on_gpu(x, "x")
+    tokens, top_k, experts, places, ends = _route(position, offsets, index)
+    ldx = _sorted(x, "x", tokens, index)
+    width, dtype = x.shape[1], x.dtype
+    out, ldo = _output(out, tokens * top_k, width, dtype, index, "out")
     code = iq.load().iq_expert_dispatch(
-        _DTYPES[x.dtype], x.data_ptr(), ldx, tokens, width, position.data_ptr(), top_k,
-        offsets.data_ptr(), experts, out.data_ptr(), ldo, _stream(index))
+        _DTYPES[dtype], x.data_ptr(), ldx, tokens, width, places, top_k, ends, experts,
+        out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_dispatch")
     return out
-
-
-def _sorted(t, name, tokens, top_k):
-    ld = _matrix(t, name)
-    if t.shape[0] != tokens * top_k:
-        raise ValueError("%s must have %d rows" % (name, tokens * top_k))
-    return ld
 
 
 def expert_dispatch_backward(grad, position, offsets, *, out=None):
     """The gradient of ``expert_dispatch``: for the gradient of its result, that
     of ``x``, the sum over each token's kept choices."""
-    tokens, top_k, experts = _route(position, offsets)
-    ldg = _sorted(grad, "grad", tokens, top_k)
-    width = grad.shape[1]
-    index = _same_device(grad, position, offsets, out)
-    out, ldo = _output(out, tokens, width, grad.dtype, grad.device, "out")
+    index = _on_gpu(grad, "grad")
+    tokens, top_k, experts, places, ends = _route(position, offsets, index)
+    ldg = _sorted(grad, "grad", tokens * top_k, index)
+    width, dtype = grad.shape[1], grad.dtype
+    out, ldo = _output(out, tokens, width, dtype, index, "out")
     code = iq.load().iq_expert_dispatch_backward(
-        _DTYPES[grad.dtype], grad.data_ptr(), ldg, tokens, width, position.data_ptr(), top_k,
-        offsets.data_ptr(), experts, out.data_ptr(), ldo, _stream(index))
+        _DTYPES[dtype], grad.data_ptr(), ldg, tokens, width, places, top_k, ends, experts,
+        out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_dispatch_backward")
     return out
 
@@ -315,15 +334,15 @@ def expert_dispatch_backward(grad, position, offsets, *, out=None):
 def expert_combine(y, position, offsets, weights, *, out=None):
     """Rows brought back to their tokens: out[t] = the sum over the kept choices
     j of weights[t, j] * y[position[t, j]] (``weights`` fp32 [tokens, top_k])."""
-    tokens, top_k, experts = _route(position, offsets)
-    ldy = _sorted(y, "y", tokens, top_k)
-    width = y.shape[1]
-    _vector(weights, torch.float32, position.shape, "weights")
-    index = _same_device(y, position, offsets, weights, out)
-    out, ldo = _output(out, tokens, width, y.dtype, y.device, "out")
+    index = _on_gpu(y, "y")
+    tokens, top_k, experts, places, ends = _route(position, offsets, index)
+    ldy = _sorted(y, "y", tokens * top_k, index)
+    width, dtype = y.shape[1], y.dtype
+    factors = _vector(weights, torch.float32, position.shape, "weights", index)
+    out, ldo = _output(out, tokens, width, dtype, index, "out")
     code = iq.load().iq_expert_combine(
-        _DTYPES[y.dtype], y.data_ptr(), ldy, tokens, width, position.data_ptr(), top_k,
-        offsets.data_ptr(), experts, weights.data_ptr(), out.data_ptr(), ldo, _stream(index))
+        _DTYPES[dtype], y.data_ptr(), ldy, tokens, width, places, top_k, ends, experts, factors,
+        out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_combine")
     return out
 
@@ -331,19 +350,18 @@ def expert_combine(y, position, offsets, weights, *, out=None):
 def expert_combine_backward(grad, y, position, offsets, weights):
     """The gradients of ``expert_combine`` for the gradient ``grad`` [tokens,
     width] of its result: (that of ``y``, that of ``weights``)."""
-    tokens, top_k, experts = _route(position, offsets)
-    ldy = _sorted(y, "y", tokens, top_k)
-    width = y.shape[1]
-    ldo = _matrix(grad, "grad", y.dtype)
+    index = _on_gpu(y, "y")
+    tokens, top_k, experts, places, ends = _route(position, offsets, index)
+    ldy = _sorted(y, "y", tokens * top_k, index)
+    width, dtype = y.shape[1], y.dtype
+    ldo = _matrix(grad, "grad", index, dtype)
     if grad.shape != (tokens, width):
         raise ValueError("grad must be [%d, %d]" % (tokens, width))
-    _vector(weights, torch.float32, position.shape, "weights")
-    index = _same_device(y, grad, position, offsets, weights)
-    y_grad = torch.empty((tokens * top_k, width), dtype=y.dtype, device=y.device)
-    weights_grad = torch.empty((tokens, top_k), dtype=torch.float32, device=y.device)
+    factors = _vector(weights, torch.float32, position.shape, "weights", index)
+    y_grad = torch.empty((tokens * top_k, width), dtype=dtype, device=_DEVICES[index])
+    weights_grad = torch.empty((tokens, top_k), dtype=torch.float32, device=_DEVICES[index])
     code = iq.load().iq_expert_combine_backward(
-        _DTYPES[y.dtype], grad.data_ptr(), ldo, y.data_ptr(), ldy, tokens, width,
-        position.data_ptr(), top_k, offsets.data_ptr(), experts, weights.data_ptr(),
-        y_grad.data_ptr(), width, weights_grad.data_ptr(), _stream(index))
+        _DTYPES[dtype], grad.data_ptr(), ldo, y.data_ptr(), ldy, tokens, width, places, top_k,
+        ends, experts, factors, y_grad.data_ptr(), width, weights_grad.data_ptr(), _stream(index))
     iq._check(code, "iq_expert_combine_backward")
     return y_grad, weights_grad
