@@ -10,6 +10,8 @@
 // channels of one token and go out as one store.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "iq_layers.h"
 #include "layers_common.hpp"
 #include "layers_launch.hpp"
@@ -55,7 +57,7 @@ template <int kRows>
 __device__ __forceinline__ Tile dense_tile(const Int8Product& p, int channel_tiles)
 {
     // Bands of kBand row tiles, channel tile by channel tile.
-    constexpr int kBand = 4;
+    constexpr int kBand = 8;
     const int64_t row_tiles = (p.rows + kRows - 1) / kRows;
     const int64_t id = by_xcd(blockIdx.x, row_tiles * channel_tiles);
     const int64_t band = id / (kBand * (int64_t)channel_tiles);
@@ -71,50 +73,52 @@ __device__ __forceinline__ Tile dense_tile(const Int8Product& p, int channel_til
 
 // Tiles of each expert one after another; the grid is as large as any
 // distribution of the rows could need, and the rest of it ends at once.  Every
-// wave finds its tile by itself, 64 segments at a time.
+// wave finds its tile by itself: lane l counts the tiles of segment l, and the
+// counts are summed up across the lanes, 64 segments at a time (up to 63
+// experts the offsets are read once).
 template <int kRows>
 __device__ __forceinline__ Tile expert_tile(const Int8Product& p, int channel_tiles)
 {
     const int lane = threadIdx.x % kWave;
-    int64_t total = 0;
-    for (int e0 = 0; e0 <= p.experts; e0 += kWave) {
+    int64_t lo = 0, hi = 0;
+    int count = 0, last = 0;          // of this lane's segment, and up to it
+    auto count_from = [&](int e0) {
         const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
+        lo = hi = 0;
         if (e <= p.experts) segment(p, e, &lo, &hi);
-        int count = hi > lo ? (int)((hi - lo + kRows - 1) / kRows) : 0;
-#pragma unroll
-        for (int d = kWave / 2; d; d >>= 1) count += __shfl_xor(count, d);
-        total += count;
-    }
-    Tile t = {0, 0, 0, -2};
-    if ((int64_t)blockIdx.x >= total * channel_tiles) return t;
-    const int64_t id = by_xcd(blockIdx.x, total * channel_tiles);
-    const int64_t row_tile = id / channel_tiles;
-    t.channel_tile = (int)(id - row_tile * channel_tiles);
-    int64_t before = 0;
-    for (int e0 = 0; e0 <= p.experts; e0 += kWave) {
-        const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (e <= p.experts) segment(p, e, &lo, &hi);
-        const int count = hi > lo ? (int)((hi - lo + kRows - 1) / kRows) : 0;
-        int sum = count;
+        count = hi > lo ? (int)((hi - lo + kRows - 1) / kRows) : 0;
+        last = count;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
+            const int up = __shfl_up(last, d);
+            if (lane >= d) last += up;
         }
-        const int64_t first = before + sum - count;
+        return __shfl(last, kWave - 1);
+    };
+    int total = count_from(0);
+    if (p.experts >= kWave) {
+        for (int e0 = kWave; e0 <= p.experts; e0 += kWave) total += count_from(e0);
+    }
+    Tile t = {0, 0, 0, -2};
+    const int64_t tiles = (int64_t)total * channel_tiles;
+    if ((int64_t)blockIdx.x >= tiles) return t;
+    const int64_t id = by_xcd(blockIdx.x, tiles);
+    const int row_tile = (int)(id / channel_tiles);
+    t.channel_tile = (int)(id - (int64_t)row_tile * channel_tiles);
+    int before = 0;
+    for (int e0 = 0; e0 <= p.experts; e0 += kWave) {
+        const int all = p.experts >= kWave ? count_from(e0) : total;
+        const int first = before + last - count;
         const uint64_t mine = __ballot(row_tile >= first && row_tile < first + count);
         if (mine) {
             const int l = __ffsll((unsigned long long)mine) - 1;
-            const int64_t at = row_tile - __shfl((int)first, l);
+            const int at = row_tile - __shfl(first, l);
             t.expert = e0 + l < p.experts ? e0 + l : -1;
-            segment(p, e0 + l, &lo, &hi);
-            t.row0 = lo + at * kRows;
-            t.row_end = hi;
+            t.row0 = (int64_t)__shfl((int)lo, l) + (int64_t)at * kRows;
+            t.row_end = __shfl((int)hi, l);
             return t;
         }
-        before += __shfl(sum, kWave - 1);
+        before += all;
     }
     return t;
 }
@@ -230,8 +234,8 @@ __device__ __forceinline__ void wait_and_meet()
 // leaves beyond whole steps has a buffer of its own, filled at the start.
 //
 // kDirect: rows start on 16 bytes, and pieces are copied straight into LDS,
-// kStages - 1 steps ahead.  Otherwise they pass through registers, two steps
-// ahead, into two buffers.
+// kStages - 1 steps ahead.  Otherwise they pass through registers, four
+// steps ahead, into two buffers.
 //
 // kPingPong (8 waves, two on a SIMD): the second four waves run half a step
 // behind, so on each SIMD one wave multiplies while the other reads its
@@ -388,7 +392,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
             }
         }
     } else {
-        uint4 passing[2][kLoads];
+        constexpr int kAhead = 4;
+        uint4 passing[kAhead][kLoads];
         auto fetch = [&](int set, int step) {
             // Beyond the last step the last one again: not used.
             const int64_t at = (int64_t)min(step, max(steps - 1, 0)) * kDepth;
@@ -396,26 +401,26 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
             for (int i = 0; i < kLoads; ++i) passing[set][i] = load16(from[i] + at);
         };
         if (steps > 0) {
-            fetch(0, 0);
-            fetch(1, 1);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(i, i);
         }
         stage_rest();
-        for (int s0 = 0; s0 < steps; s0 += 2) {
+        for (int s0 = 0; s0 < steps; s0 += kAhead) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kAhead; ++u) {
                 const int s = s0 + u;
                 if (s >= steps) break;
-                // Buffer u was last read in step s - 2, before the last barrier.
+                // This buffer was last read in step s - 2, before the last barrier.
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i)
-                    *reinterpret_cast<uint4*>(&staged[u][(wave * kLoads + i) * 1024 + lane * 16]) =
-                        passing[u][i];
+                    *reinterpret_cast<uint4*>(
+                        &staged[u % 2][(wave * kLoads + i) * 1024 + lane * 16]) = passing[u][i];
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                fetch(u, s + 2);
+                fetch(u, s + kAhead);
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) {
                     v4i a[kFC], x[kFT];
-                    read(u, k, a, x);
+                    read(u % 2, k, a, x);
                     multiply(a, x);
                 }
             }
@@ -528,46 +533,102 @@ hipError_t launch_tiles(const Int8Product& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-// The expected time of a tile size, in units of a step over 4096 of the depth:
-// every compute unit takes its tiles one after another, or two at once where
-// two fit its LDS.  one, two: measured microseconds of one tile and of two at
-// once, at a depth of 4096.
-double tile_cost(const Int8Product& p, int cus, int rows, int channels, double one, double two)
+// The expected time of a tile size in microseconds.  Compute units take their
+// tiles one after another, each costing `start` for its first loads and its
+// results, and `depth` for every 1024 of the depth, plus `full` of that in the
+// measure in which all units are busy (the matrix cores then share the card's
+// power).  Of the small tiles two fit a unit's LDS at once: each pair costs
+// `start` and `depth`, a single one `start1` and `depth1`.  `once` is what the
+// whole product costs beside them.
+struct TileTime {
+    int rows, channels;
+    bool pairs;
+    double once, start, depth, full, start1, depth1;
+};
+
+double expected_time(const Int8Product& p, int cus, const TileTime& t)
 {
-    double row_tiles = (double)((p.rows + rows - 1) / rows);
+    double row_tiles = (double)((p.rows + t.rows - 1) / t.rows);
     if (p.experts) {
-        // Rows spread over the experts: each that has any ends in half a tile.
-        const double used = p.rows < p.experts ? (double)p.rows : (double)p.experts;
-        row_tiles = (double)p.rows / rows + 0.5 * used;
-        if (row_tiles < used) row_tiles = used;
+        // As if every row chose its expert evenly: the last tile of an expert
+        // that has rows is half full.
+        const double each = (double)p.rows / p.experts;
+        const double used = p.experts * (1.0 - exp(-each));
+        row_tiles = fmax(used, (double)p.rows / t.rows + 0.5 * used);
     }
-    const double tiles = row_tiles * (double)((p.channels + channels - 1) / channels);
-    const int64_t each = (int64_t)((tiles + cus - 1) / cus);
-    return two > 0.0 ? (double)(each / 2) * two + (double)(each % 2) * one : (double)each * one;
+    const double tiles = row_tiles * ((p.channels + t.channels - 1) / t.channels);
+    const double each = ceil(tiles / cus), k = p.depth / 1024.0;
+    if (t.pairs) {
+        const double pairs = floor(0.5 * each), single = each - 2.0 * pairs;
+        return t.once + pairs * (t.start + t.depth * k) + single * (t.start1 + t.depth1 * k);
+    }
+    return t.once + each * (t.start + t.depth * k) + t.full * k * tiles / cus;
+}
+
+// Fitted to the times of every tile in 240 products of 1 to 4096 tokens, 256 to
+// 5632 channels and depths of 512 to 5632.  The tile with the least expected
+// time took 1 % longer than the fastest of ten sizes on average (128 x 128
+// alone: 30 %).
+constexpr TileTime kDense[] = {
+    {32, 32, true, 3.1, 1.40, 1.27, 0.0, 0.0, 1.28},
+    {64, 64, true, 3.3, 2.36, 2.65, 0.0, 2.80, 1.47},
+    {64, 128, false, 2.1, 3.38, 1.88, 0.52, 0.0, 0.0},
+    {128, 128, false, 1.4, 4.58, 2.63, 1.03, 0.0, 0.0},
+    {128, 256, false, 0.0, 5.67, 5.12, 3.89, 0.0, 0.0},
+    {256, 256, false, 0.0, 9.77, 6.87, 7.01, 0.0, 0.0}};
+// Likewise for products by expert, 1 to 4096 tokens of 2 and 8 choices, 8, 16
+// and 64 experts, chosen evenly and not: 4 % longer than the fastest.  A tile
+// starts later than in a dense product, its weight coming from HBM.
+constexpr TileTime kByExpert[] = {
+    {32, 32, true, 4.6, 4.29, 1.29, 0.0, 0.49, 1.81},
+    {64, 64, true, 4.1, 5.77, 2.79, 0.0, 3.93, 1.42},
+    {128, 128, false, 3.1, 6.67, 1.09, 2.94, 0.0, 0.0},
+    {128, 256, false, 1.1, 7.80, 3.39, 6.01, 0.0, 0.0},
+    {256, 256, false, 0.6, 10.38, 5.70, 6.83, 0.0, 0.0}};
+// And where rows do not start on 16 bytes: 1 % longer than the fastest.
+constexpr TileTime kUnaligned[] = {
+    {32, 32, true, 6.7, 2.88, 2.19, 0.0, 0.70, 2.08},
+    {64, 64, true, 2.7, 8.51, 4.96, 0.0, 5.90, 2.84},
+    {128, 128, false, 1.3, 10.82, 5.18, 1.52, 0.0, 0.0}};
+
+// The rows and channels of the entry with the least expected time.
+template <int kN>
+int choose_tile(const Int8Product& p, int cus, const TileTime (&tiles)[kN])
+{
+    int best = 0;
+    double least = expected_time(p, cus, tiles[0]);
+    for (int i = 1; i < kN; ++i) {
+        const double time = expected_time(p, cus, tiles[i]);
+        if (time < least) {
+            least = time;
+            best = i;
+        }
+    }
+    return tiles[best].rows * 1000 + tiles[best].channels;
 }
 
 }  // namespace
 
-// Which tile: the one with the least expected time.
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream)
 {
     const bool direct = p.ldx % 16 == 0 && p.ldw % 16 == 0 && p.w_stride % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
-    const double t32 = tile_cost(p, cus, 32, 32, 5.5, 8.2);
-    const double t64 = tile_cost(p, cus, 64, 64, 9.3, 14.0);
-    const double t128 = tile_cost(p, cus, 128, 128, 17.0, 0.0);
-    const double t256 = tile_cost(p, cus, 256, 256, 48.0, 0.0);
     if (!direct) {
-        if (t32 <= t64 && t32 <= t128) return launch_tiles<32, 32, 2, 2, 256, 2, false, false>(p, stream);
-        if (t64 <= t128) return launch_tiles<64, 64, 2, 2, 128, 2, false, false>(p, stream);
-        return launch_tiles<128, 128, 2, 2, 128, 2, false, false>(p, stream);
+        switch (choose_tile(p, cus, kUnaligned)) {
+        case 32032: return launch_tiles<32, 32, 2, 2, 128, 2, false, false>(p, stream);
+        case 64064: return launch_tiles<64, 64, 4, 2, 128, 2, false, false>(p, stream);
+        default: return launch_tiles<128, 128, 4, 4, 128, 2, false, false>(p, stream);
+        }
     }
-    if (t32 <= t64 && t32 <= t128 && t32 <= t256)
-        return launch_tiles<32, 32, 2, 2, 256, 4, false, true>(p, stream);
-    if (t64 <= t128 && t64 <= t256) return launch_tiles<64, 64, 2, 2, 128, 4, false, true>(p, stream);
-    if (t128 <= t256) return launch_tiles<128, 128, 4, 2, 128, 4, true, true>(p, stream);
-    return launch_tiles<256, 256, 4, 2, 64, 4, true, true>(p, stream);
+    switch (p.experts ? choose_tile(p, cus, kByExpert) : choose_tile(p, cus, kDense)) {
+    case 32032: return launch_tiles<32, 32, 2, 2, 256, 4, false, true>(p, stream);
+    case 64064: return launch_tiles<64, 64, 2, 2, 128, 4, false, true>(p, stream);
+    case 64128: return launch_tiles<64, 128, 2, 4, 128, 4, true, true>(p, stream);
+    case 128128: return launch_tiles<128, 128, 4, 2, 128, 4, true, true>(p, stream);
+    case 128256: return launch_tiles<128, 256, 2, 4, 64, 4, true, true>(p, stream);
+    default: return launch_tiles<256, 256, 4, 2, 64, 4, true, true>(p, stream);
+    }
 }
 
 }  // namespace iqk
