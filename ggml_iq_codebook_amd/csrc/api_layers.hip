@@ -49,6 +49,13 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // The codes of iq_int8_linear: rows that start on 16 bytes.
 int64_t code_stride(int64_t depth) { return round_up(depth, 16); }
 
+iqk::Route route(iq_dtype_t dtype, int64_t tokens, int64_t width, const int32_t* position,
+                 int32_t top_k, const int32_t* offsets, int32_t experts)
+{
+    return {tokens, width, position, top_k, offsets + experts,
+            iqk::streams(tokens * top_k, width, value_bytes(dtype))};
+}
+
 // One tensor of a routing call: [tokens][width], or [tokens * top_k][width]
 // where it is sorted.
 struct Rows {
@@ -230,7 +237,7 @@ iq_status_t iq_expert_dispatch(iq_dtype_t dtype, const void* x, int64_t ldx, int
     if (st || !tokens) return st;
     st = check_device();
     if (st) return st;
-    const iqk::Route r = {tokens, width, position, top_k, offsets + experts};
+    const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
     return from_hip(iqk::launch_expert_dispatch(dtype, r, x, ldx, sorted, lds, stream));
 }
 
@@ -244,7 +251,7 @@ iq_status_t iq_expert_dispatch_backward(iq_dtype_t dtype, const void* sorted_gra
     if (st || !tokens) return st;
     st = check_device();
     if (st) return st;
-    const iqk::Route r = {tokens, width, position, top_k, offsets + experts};
+    const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
     return from_hip(iqk::launch_expert_combine(dtype, r, sorted_grad, lds, nullptr, x_grad, ldx,
                                                stream));
 }
@@ -262,7 +269,7 @@ iq_status_t iq_expert_combine(iq_dtype_t dtype, const void* y, int64_t ldy, int6
     if (!tokens) return IQ_OK;
     st = check_device();
     if (st) return st;
-    const iqk::Route r = {tokens, width, position, top_k, offsets + experts};
+    const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
     return from_hip(iqk::launch_expert_combine(dtype, r, y, ldy, weights, out, ldo, stream));
 }
 
@@ -282,7 +289,7 @@ iq_status_t iq_expert_combine_backward(iq_dtype_t dtype, const void* out_grad, i
     if (!tokens) return IQ_OK;
     st = check_device();
     if (st) return st;
-    const iqk::Route r = {tokens, width, position, top_k, offsets + experts};
+    const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
     return from_hip(iqk::launch_expert_combine_backward(dtype, r, out_grad, ldo, y, ldy, weights,
                                                         y_grad, ldg, weights_grad, stream));
 }

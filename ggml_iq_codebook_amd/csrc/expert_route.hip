@@ -28,7 +28,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kMaxKeys = IQ_MAX_EXPERTS + 1;
 static_assert(kMaxKeys <= kSortThreads, "a thread per key");
-constexpr int64_t kChunkChoices = 4096;
+constexpr int kKeptSteps = 4;         // steps of 64 choices a wave keeps in registers
+constexpr int64_t kAloneChoices = (int64_t)kKeptSteps * kSortThreads;
 constexpr int kMaxChunks = 256;
 
 // The choice at place i as a key 0..experts, experts where it is dropped.
@@ -60,10 +61,25 @@ __global__ __launch_bounds__(kSortThreads) void expert_count_kernel(
         counts[(int64_t)blockIdx.x * (experts + 1) + e] = count[e];
 }
 
-// Places a chunk's choices.  Each wave takes a consecutive part of the chunk
-// and counts it in a row of its own, so the ranks follow the order of the
-// choices: chunk, wave, step of 64, lane.
-template <class Choice>
+// The lanes of a wave that hold the same key (of the live ones), found bit by
+// bit.
+__device__ __forceinline__ uint64_t same_key(int key, bool live, int bits)
+{
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((key >> b) & 1);
+        same &= ((key >> b) & 1) ? set : ~set;
+    }
+    return same;
+}
+
+// Places a chunk's choices.  Each wave takes a consecutive part of the chunk,
+// so the ranks follow the order of the choices: chunk, wave, step of 64, lane.
+// A wave first ranks each choice among the equal ones of its own part, in a row
+// of counters of its own; what the keys, chunks and waves before it hold is
+// added afterwards.  kKept: the part is at most kKeptSteps steps, and keys and
+// ranks stay in registers in between; otherwise they are found again.
+template <class Choice, bool kKept>
 __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(
     const Choice* __restrict__ choice, int64_t n, int64_t per_chunk, int experts,
     const int32_t* __restrict__ counts, int32_t* __restrict__ order,
@@ -71,24 +87,57 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(
 {
     extern __shared__ int32_t shared[];
     const int keys = experts + 1;
-    int32_t* before = shared;                     // [waves][keys]: then the next place
+    int32_t* before = shared;                     // [waves][keys]: counters, then first places
     int32_t* total = shared + kSortWaves * keys;  // [keys]: over all chunks
     int32_t* start = total + keys;                // [keys]: of the chunks before this one
     __shared__ int32_t wave_sums[kSortWaves];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int64_t first = blockIdx.x * per_chunk;
     const int64_t last = min(first + per_chunk, n);
-
-    for (int i = threadIdx.x; i < (kSortWaves + 2) * keys; i += kSortThreads) shared[i] = 0;
-    __syncthreads();
-
-    // This chunk's keys, counted per wave.
     const int64_t per_wave = ((per_chunk + kSortThreads - 1) / kSortThreads) * kWave;
     const int64_t wfirst = first + wave * per_wave;
     const int64_t wlast = min(wfirst + per_wave, last);
+    const int steps = wlast > wfirst ? (int)((wlast - wfirst + kWave - 1) / kWave) : 0;
+    const uint64_t below = (1ull << lane) - 1ull;
+    int bits = 0;
+    while ((1 << bits) < keys) ++bits;
+
+    int key[kKeptSteps], rank[kKeptSteps];
     bool bad = false;
-    for (int64_t i = wfirst + lane; i < wlast; i += kWave)
-        atomicAdd(&before[wave * keys + key_of(choice, i, experts, &bad)], 1);
+    if (kKept) {
+#pragma unroll
+        for (int s = 0; s < kKeptSteps; ++s) {
+            const int64_t i = wfirst + s * kWave + lane;
+            key[s] = i < wlast ? key_of(choice, i, experts, &bad) : -1;
+        }
+    }
+    for (int i = threadIdx.x; i < (kSortWaves + 2) * keys; i += kSortThreads) shared[i] = 0;
+    __syncthreads();
+
+    // One step's rank among the wave's earlier choices of the same key.  All
+    // lanes read a counter before its first lane advances it: a wave's LDS
+    // accesses are done in order.
+    int32_t* mine = before + wave * keys;
+    auto rank_of = [&](int k, bool live) {
+        const uint64_t same = same_key(k, live, bits);
+        const int32_t base = live ? mine[k] : 0;
+        const int32_t r = __popcll(same & below);
+        __builtin_amdgcn_wave_barrier();
+        if (live && r == 0) mine[k] = base + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        return base + r;
+    };
+    if (kKept) {
+#pragma unroll
+        for (int s = 0; s < kKeptSteps; ++s)
+            if (s < steps) rank[s] = rank_of(max(key[s], 0), key[s] >= 0);
+    } else {
+        for (int s = 0; s < steps; ++s) {
+            const int64_t i = wfirst + (int64_t)s * kWave + lane;
+            const bool live = i < wlast;
+            rank_of(live ? key_of(choice, i, experts, &bad) : 0, live);
+        }
+    }
     if (bad) report_generic(status, IQ_ERR_INDEX);
     // The other chunks' counts: several threads a key, each over some chunks.
     if (gridDim.x > 1) {
@@ -106,19 +155,19 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(
         }
     }
     __syncthreads();
-    if (gridDim.x == 1) {
-        for (int e = threadIdx.x; e < keys; e += kSortThreads) {
-            int32_t all = 0;
-            for (int w = 0; w < kSortWaves; ++w) all += before[w * keys + e];
-            total[e] = all;
-        }
-        __syncthreads();
-    }
     // First place of each key: the sum over the keys before it.
     {
         const int e = threadIdx.x;
-        const int32_t mine = e < keys ? total[e] : 0;
-        int32_t sum = mine;
+        int32_t held[kSortWaves], here = 0;
+        if (e < keys) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) {
+                held[w] = before[w * keys + e];
+                here += held[w];
+            }
+        }
+        const int32_t all = e < keys ? (gridDim.x > 1 ? total[e] : here) : 0;
+        int32_t sum = all;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
             const int32_t up = __shfl_up(sum, d);
@@ -126,44 +175,38 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(
         }
         if (lane == kWave - 1) wave_sums[wave] = sum;
         __syncthreads();
-        int32_t place = sum - mine;
-        for (int w = 0; w < wave; ++w) place += wave_sums[w];
         if (e < keys) {
-            if (blockIdx.x == 0) offsets[e] = place;
+            int32_t next = sum - all;
+            for (int w = 0; w < wave; ++w) next += wave_sums[w];
+            if (blockIdx.x == 0) offsets[e] = next;
             // and of this chunk's waves
-            int32_t next = place + start[e];
+            next += start[e];
+#pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
-                const int32_t c = before[w * keys + e];
                 before[w * keys + e] = next;
-                next += c;
+                next += held[w];
             }
         }
         __syncthreads();
     }
-    // Ranks: lanes with the same key find each other bit by bit.
-    int bits = 0;
-    while ((1 << bits) < keys) ++bits;
-    const uint64_t below = (1ull << lane) - 1ull;
-    for (int64_t i0 = wfirst; i0 < wlast; i0 += kWave) {
-        const int64_t i = i0 + lane;
-        const bool live = i < wlast;
-        const int key = live ? key_of(choice, i, experts, &bad) : 0;
-        uint64_t same = __ballot(live);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((key >> b) & 1);
-            same &= ((key >> b) & 1) ? set : ~set;
-        }
-        int32_t* next = &before[wave * keys + key];
-        const int32_t base = live ? *next : 0;
-        const int32_t rank = __popcll(same & below);
-        // All lanes have read the row's counter before its first lane advances
-        // it: a wave's LDS accesses are done in order.
-        __builtin_amdgcn_wave_barrier();
-        if (live && rank == 0) *next = base + __popcll(same);
-        __builtin_amdgcn_wave_barrier();
-        if (live) {
-            position[i] = base + rank;
-            order[base + rank] = (int32_t)i;
+    if (kKept) {
+#pragma unroll
+        for (int s = 0; s < kKeptSteps; ++s)
+            if (key[s] >= 0) {
+                const int64_t i = wfirst + s * kWave + lane;
+                const int32_t place = mine[key[s]] + rank[s];
+                position[i] = place;
+                order[place] = (int32_t)i;
+            }
+    } else {
+        for (int s = 0; s < steps; ++s) {
+            const int64_t i = wfirst + (int64_t)s * kWave + lane;
+            const bool live = i < wlast;
+            const int32_t place = rank_of(live ? key_of(choice, i, experts, &bad) : 0, live);
+            if (live) {
+                position[i] = place;
+                order[place] = (int32_t)i;
+            }
         }
     }
 }
@@ -199,7 +242,7 @@ __device__ __forceinline__ int64_t token_of(int lanes)
            (kWaves ? __builtin_amdgcn_readfirstlane(in_block) : in_block);
 }
 
-template <int kDT, bool kWaves>
+template <int kDT, bool kWaves, bool kStreaming>
 __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
                                                                    const void* __restrict__ x,
                                                                    int64_t ldx,
@@ -221,9 +264,9 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(Route r,
             if (p < 0) continue;
             raw* to = static_cast<raw*>(sorted) + p * lds;
             if (p < kept)
-                v.store(to, at, r.width);
+                v.template store<kStreaming>(to, at, r.width);
             else
-                none.store(to, at, r.width);
+                none.template store<kStreaming>(to, at, r.width);
         }
     }
 }
@@ -316,7 +359,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(Route r,
 // A token's gradient is scaled into the rows of its choices, and multiplied
 // with what those rows held, kGroup choices at a time.  kLanes: a wave or the
 // workgroup shares a token.
-template <int kDT, int kLanes>
+template <int kDT, int kLanes, bool kStreaming>
 __global__ __launch_bounds__(kThreads) void expert_combine_backward_kernel(
     Route r, const void* __restrict__ out_grad, int64_t ldo, const void* __restrict__ y,
     int64_t ldy, const float* __restrict__ weights, void* __restrict__ y_grad, int64_t ldg,
@@ -347,7 +390,8 @@ __global__ __launch_bounds__(kThreads) void expert_combine_backward_kernel(
                     }
                 }
                 if (c.place[g] >= 0)
-                    d.store(static_cast<raw*>(y_grad) + c.place[g] * ldg, at, r.width);
+                    d.template store<kStreaming>(static_cast<raw*>(y_grad) + c.place[g] * ldg, at,
+                                                 r.width);
             };
             Row<kDT> grad;
             grad.load(gr, at, r.width);
@@ -404,15 +448,29 @@ int lanes_for(int64_t width, int values)
 
 }  // namespace
 
+// One workgroup while a wave's part fits its registers; beyond, a workgroup per
+// 1024 choices, or more where that would be over 256 of them.
 SortPlan expert_sort_plan(int64_t n)
 {
     SortPlan s;
-    s.per_chunk = kChunkChoices;
+    s.per_chunk = n <= kAloneChoices ? kAloneChoices : kSortThreads;
     if ((n + s.per_chunk - 1) / s.per_chunk > kMaxChunks)
         s.per_chunk = ((n + kMaxChunks - 1) / kMaxChunks + kSortThreads - 1) / kSortThreads *
                       kSortThreads;
     s.chunks = (int)((n + s.per_chunk - 1) / s.per_chunk);
+    if (s.chunks <= 1) s.per_chunk = (n + kSortThreads - 1) / kSortThreads * kSortThreads;
     return s;
+}
+
+template <class Choice, bool kKept>
+static void place_as(const SortPlan& s, const Choice* choice, int64_t n, int experts,
+                     int32_t* order, int32_t* position, int32_t* offsets, int32_t* counts,
+                     int32_t* status, hipStream_t stream)
+{
+    const size_t lds = sizeof(int32_t) * (kSortWaves + 2) * (experts + 1);
+    hipLaunchKernelGGL((expert_place_kernel<Choice, kKept>), dim3(s.chunks), dim3(kSortThreads),
+                       lds, stream, choice, n, s.per_chunk, experts, counts, order, position,
+                       offsets, status);
 }
 
 template <class Choice>
@@ -425,10 +483,10 @@ static hipError_t sort_as(const void* choice, int64_t n, int experts, int32_t* o
     if (s.chunks > 1)
         hipLaunchKernelGGL((expert_count_kernel<Choice>), dim3(s.chunks), dim3(kSortThreads), 0,
                            stream, c, n, s.per_chunk, experts, counts);
-    const size_t lds = sizeof(int32_t) * (kSortWaves + 2) * (experts + 1);
-    hipLaunchKernelGGL((expert_place_kernel<Choice>), dim3(s.chunks), dim3(kSortThreads), lds,
-                       stream, c, n, s.per_chunk, experts, counts, order, position, offsets,
-                       status);
+    if (s.per_chunk <= kAloneChoices)
+        place_as<Choice, true>(s, c, n, experts, order, position, offsets, counts, status, stream);
+    else
+        place_as<Choice, false>(s, c, n, experts, order, position, offsets, counts, status, stream);
     return hipGetLastError();
 }
 
@@ -454,12 +512,11 @@ hipError_t launch_expert_dispatch(int dtype, const Route& r, const void* x, int6
         constexpr int kDT = decltype(dt)::value;
         const int lanes = lanes_for(r.width, Row<kDT>::kN);
         const dim3 wgs((unsigned)((r.tokens + kThreads / lanes - 1) / (kThreads / lanes)));
-        if (lanes >= kWave)
-            hipLaunchKernelGGL((expert_dispatch_kernel<kDT, true>), wgs, dim3(kThreads), 0, stream,
-                               r, x, ldx, sorted, lds, lanes);
-        else
-            hipLaunchKernelGGL((expert_dispatch_kernel<kDT, false>), wgs, dim3(kThreads), 0,
-                               stream, r, x, ldx, sorted, lds, lanes);
+        const auto kernel = lanes < kWave ? (r.streaming ? expert_dispatch_kernel<kDT, false, true>
+                                                         : expert_dispatch_kernel<kDT, false, false>)
+                                          : (r.streaming ? expert_dispatch_kernel<kDT, true, true>
+                                                         : expert_dispatch_kernel<kDT, true, false>);
+        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, r, x, ldx, sorted, lds, lanes);
         return hipGetLastError();
     });
 }
@@ -508,16 +565,16 @@ hipError_t launch_expert_combine_backward(int dtype, const Route& r, const void*
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
         // Two vectors a lane of a wave at most, else the workgroup.
-        if (r.width <= 2 * kWave * Row<kDT>::kN) {
-            const dim3 wgs((unsigned)((r.tokens + kThreads / kWave - 1) / (kThreads / kWave)));
-            hipLaunchKernelGGL((expert_combine_backward_kernel<kDT, kWave>), wgs, dim3(kThreads),
-                               0, stream, r, out_grad, ldo, y, ldy, weights, y_grad, ldg,
-                               weights_grad);
-        } else {
-            hipLaunchKernelGGL((expert_combine_backward_kernel<kDT, kThreads>),
-                               dim3((unsigned)r.tokens), dim3(kThreads), 0, stream, r, out_grad,
-                               ldo, y, ldy, weights, y_grad, ldg, weights_grad);
-        }
+        const bool by_wave = r.width <= 2 * kWave * Row<kDT>::kN;
+        constexpr int kTokens = kThreads / kWave;
+        const dim3 wgs((unsigned)(by_wave ? (r.tokens + kTokens - 1) / kTokens : r.tokens));
+        const auto kernel =
+            by_wave ? (r.streaming ? expert_combine_backward_kernel<kDT, kWave, true>
+                                   : expert_combine_backward_kernel<kDT, kWave, false>)
+                    : (r.streaming ? expert_combine_backward_kernel<kDT, kThreads, true>
+                                   : expert_combine_backward_kernel<kDT, kThreads, false>);
+        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, r, out_grad, ldo, y, ldy,
+                           weights, y_grad, ldg, weights_grad);
         return hipGetLastError();
     });
 }

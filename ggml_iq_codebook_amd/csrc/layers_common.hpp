@@ -82,6 +82,18 @@ struct Row {
                 if (at + i < width) row[at + i] = get(i);
         }
     }
+    // kStreaming: a whole vector goes past the caches.
+    template <bool kStreaming>
+    __device__ __forceinline__ void store(raw* row, int64_t at, int64_t width) const
+    {
+        if (kStreaming && at + kN <= width) {
+            typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+            const u4 v = {u[0], u[1], u[2], u[3]};
+            __builtin_nontemporal_store(v, reinterpret_cast<u4*>(row + at));
+        } else {
+            store(row, at, width);
+        }
+    }
     __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0u; }
     // Value i of a vector that held 0 there.
     __device__ __forceinline__ void put(int i, raw r)

@@ -416,6 +416,23 @@ def test_copies_strides(dtype, width, pad, shift):
         assert (whole == 7.0).all()
 
 
+def test_copies_of_rows_larger_than_the_caches():
+    """Over 128 MiB of sorted rows: against torch's own indexing, which the copies equal."""
+    tokens, top_k, width = 9000, 3, 2603
+    c = routing(tokens, top_k, 6, 77, 0.05).to(DEV)
+    order, p, f = iq.expert_sort(c, 6)
+    kept = int(f[-1])
+    x = normal((tokens, width), 1, torch.bfloat16)
+    xs = iq.expert_dispatch(x, p, f)
+    assert torch.equal(xs[:kept], x[(order[:kept] // top_k).long()]) and not xs[kept:].any()
+    w = torch.rand((tokens, top_k), generator=gen(3)).to(DEV)
+    gy, gw = iq.expert_combine_backward(x, xs, p, f, w)
+    want = (x[(order[:kept] // top_k).long()].float() * w.flatten()[order[:kept].long()][:, None]).bfloat16()
+    assert torch.equal(gy[:kept], want) and not gy[kept:].any()
+    size = ref.to64(x.float().square().sum(1, dtype=torch.float64))[:, None] * (c >= 0).cpu().numpy()
+    within(gw, size, ref.dot_bound(size, width))
+
+
 def test_copies_skip_places_out_of_range():
     x = normal((4, 24), 1)
     p = torch.tensor([[0, -1], [99, 1], [2, 2 ** 31 - 1], [-2 ** 31, 3]], dtype=torch.int32, device=DEV)

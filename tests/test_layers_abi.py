@@ -117,7 +117,7 @@ def test_int8_expert_matmul_refusals(lib):
 
 def test_expert_sort_refusals(lib):
     assert lib.iq_expert_sort_workspace(4096, 16) == 0
-    assert lib.iq_expert_sort_workspace(4097, 16) == 2 * 17 * 4
+    assert lib.iq_expert_sort_workspace(4097, 16) == 5 * 17 * 4
     assert lib.iq_expert_sort_workspace(2 ** 31 - 1, 512) <= 256 * 513 * 4
     assert lib.iq_expert_sort_workspace(0, 16) == 0
     assert lib.iq_expert_sort_workspace(4097, 513) == 0
