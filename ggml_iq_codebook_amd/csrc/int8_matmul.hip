@@ -611,7 +611,9 @@ int choose_tile(const Int8Product& p, int cus, const TileTime (&tiles)[kN])
 
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream)
 {
-    const bool direct = p.ldx % 16 == 0 && p.ldw % 16 == 0 && p.w_stride % 16 == 0 &&
+    const bool direct = (p.tokens == 1 || p.ldx % 16 == 0) &&
+                        (p.channels == 1 || p.ldw % 16 == 0) &&
+                        (p.experts <= 1 || p.w_stride % 16 == 0) &&
                         reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
     if (!direct) {

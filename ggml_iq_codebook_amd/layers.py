@@ -282,16 +282,25 @@ def expert_sort(experts_of, num_experts, *, status=None, check=True):
     return order, position, offsets
 
 
+def _places(t, name, dims, index):
+    """The address of a contiguous int32 tensor of that many dimensions on that GPU."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _refuse(t, name, index)
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be %s, got %s" % (name, torch.int32, t.dtype))
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of %d dimensions" % (name, dims))
+    return t.data_ptr()
+
+
 def _route(position, offsets, index):
     """Checks of expert_sort's answers: (tokens, top_k, experts, their addresses)."""
-    if not isinstance(position, torch.Tensor) or position.dim() != 2:
-        raise ValueError("position must be [tokens, top_k]")
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
-        raise ValueError("offsets must be [num_experts + 1]")
+    places, ends = _places(position, "position", 2, index), _places(offsets, "offsets", 1, index)
     tokens, top_k = position.shape
-    return (tokens, top_k, offsets.shape[0] - 1,
-            _vector(position, torch.int32, position.shape, "position", index),
-            _vector(offsets, torch.int32, offsets.shape, "offsets", index))
+    experts = offsets.shape[0] - 1
+    if experts < 1:
+        raise ValueError("offsets must be [num_experts + 1]")
+    return tokens, top_k, experts, places, ends
 
 
 def _sorted(t, name, rows, index):

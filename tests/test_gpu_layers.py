@@ -585,3 +585,16 @@ def test_binding_refusals():
             (TypeError, lambda: iq.expert_combine_backward(x.half(), x, p, f, wt))]:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("fmt", ["iq1_s", "iq2_xs", "iq1_m"])
+def test_example_serves_and_trains_an_expert_layer(fmt):
+    """Rounding to 8 bits moves a code by at most half a step: an activation or weight of a
+    row whose largest is m times its root mean square is off by m / 127 / sqrt(12) of that,
+    under 1.2 % for m <= 5; both, and the roundings to bf16 (0.2 % each), stay under 3 %.
+    The training step's own gradient is exact up to bf16: three roundings of 2^-9."""
+    from examples import expert_layer
+    error, train_error, _ = expert_layer.run(experts=4, channels=96, depth=512, tokens=70, top_k=2,
+                                             fmt=fmt, repeats=2)
+    assert 0.0 < error < 0.03
+    assert train_error < 4 * 2.0 ** -9
