@@ -234,8 +234,8 @@ __device__ __forceinline__ void wait_and_meet()
 // leaves beyond whole steps has a buffer of its own, filled at the start.
 //
 // kDirect: rows start on 16 bytes, and pieces are copied straight into LDS,
-// kStages - 1 steps ahead.  Otherwise they pass through registers, four
-// steps ahead, into two buffers.
+// kStages - 1 steps ahead.  Otherwise they pass through registers, four steps
+// ahead (two for the largest tile), into two buffers.
 //
 // kPingPong (8 waves, two on a SIMD): the second four waves run half a step
 // behind, so on each SIMD one wave multiplies while the other reads its
@@ -392,7 +392,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
             }
         }
     } else {
-        constexpr int kAhead = 4;
+        // As far ahead as the registers go.
+        constexpr int kAhead = kRows * kChannels > 128 * 128 ? 2 : 4;
         uint4 passing[kAhead][kLoads];
         auto fetch = [&](int set, int step) {
             // Beyond the last step the last one again: not used.
@@ -589,7 +590,8 @@ constexpr TileTime kByExpert[] = {
 constexpr TileTime kUnaligned[] = {
     {32, 32, true, 6.7, 2.88, 2.19, 0.0, 0.70, 2.08},
     {64, 64, true, 2.7, 8.51, 4.96, 0.0, 5.90, 2.84},
-    {128, 128, false, 1.3, 10.82, 5.18, 1.52, 0.0, 0.0}};
+    {128, 128, false, 1.3, 10.82, 5.18, 1.52, 0.0, 0.0},
+    {128, 256, false, 0.0, 13.0, 12.5, 2.5, 0.0, 0.0}};
 
 // The rows and channels of the entry with the least expected time.
 template <int kN>
@@ -620,7 +622,8 @@ hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream
         switch (choose_tile(p, cus, kUnaligned)) {
         case 32032: return launch_tiles<32, 32, 2, 2, 128, 2, false, false>(p, stream);
         case 64064: return launch_tiles<64, 64, 4, 2, 128, 2, false, false>(p, stream);
-        default: return launch_tiles<128, 128, 4, 4, 128, 2, false, false>(p, stream);
+        case 128128: return launch_tiles<128, 128, 4, 4, 128, 2, false, false>(p, stream);
+        default: return launch_tiles<128, 256, 2, 4, 64, 2, false, false>(p, stream);
         }
     }
     switch (p.experts ? choose_tile(p, cus, kByExpert) : choose_tile(p, cus, kDense)) {

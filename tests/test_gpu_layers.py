@@ -170,6 +170,48 @@ def test_product_strides(tokens, pad, shift):
     assert (whole == 7.0).all()                     # nothing beside the rows was written
 
 
+# Shapes that take every tile size, with rows, channels and depths that end inside a tile.
+LARGE = [(33, 300, 528), (700, 515, 1000), (500, 2049, 528), (700, 2049, 1000), (2600, 515, 2050),
+         (1000, 2049, 1000), (2100, 2049, 528), (1300, 4100, 1000), (2600, 2049, 1000), (4100, 2049, 528),
+         (4100, 2600, 2050), (190, 4100, 528), (3300, 515, 136)]
+
+
+def exact_product(x, xs, w, ws):
+    """In 64 bits on the GPU: sums of products of 8-bit values are exact there."""
+    return (x.double() @ w.double().T) * xs.double()[:, None] * ws.double()
+
+
+@pytest.mark.parametrize("tokens,channels,depth", LARGE)
+@pytest.mark.parametrize("pad", [0, 16], ids=["dense", "padded"])
+def test_product_tiles(tokens, channels, depth, pad):
+    pad = -depth % 16 + pad if pad else 0            # padded rows start on 16 bytes
+    x, w = codes((tokens, depth + pad), 1)[:, :depth], codes((channels, depth + pad), 2)[:, :depth]
+    xs, ws = scales(tokens, 3), scales(channels, 4)
+    want = ref.to64(exact_product(x, xs, w, ws))
+    for dtype in DTYPES:
+        within(iq.int8_matmul(x, xs, w, ws, dtype=dtype), want, ref.product_bound(want, dtype))
+
+
+@pytest.mark.parametrize("tokens,channels,depth", LARGE)
+@pytest.mark.parametrize("pad", [0, 16], ids=["dense", "padded"])
+def test_expert_product_tiles(tokens, channels, depth, pad):
+    experts, top_k = 5, 2
+    pad = -depth % 16 + pad if pad else 0
+    c = routing(tokens, top_k, experts, tokens, 0.1)
+    c[tokens // 2:, 0] = torch.where(c[tokens // 2:, 0] < 0, -1, 2)     # one expert has most rows
+    order, position, offsets = (torch.tensor(v).to(DEV) for v in ref.sort(c.numpy(), experts))
+    x, w = codes((tokens, depth + pad), 1)[:, :depth], codes((experts, channels, depth + pad), 2)[:, :, :depth]
+    xs, ws = scales(tokens, 3), scales((experts, channels), 4)
+    want = torch.zeros((tokens * top_k, channels), dtype=torch.float64, device=DEV)
+    ends = offsets.tolist()
+    for e in range(experts):
+        tok = (order[ends[e]:ends[e + 1]] // top_k).long()
+        want[ends[e]:ends[e + 1]] = exact_product(x[tok], xs[tok], w[e], ws[e])
+    want = ref.to64(want)
+    y = iq.int8_expert_matmul(x, xs, w, ws, offsets, order, top_k=top_k, dtype=torch.bfloat16)
+    within(y, want, ref.product_bound(want, torch.bfloat16))
+
+
 def test_product_of_a_broadcast_row():
     x, w = codes((1, 256), 9), codes((140, 256), 10)
     xs, ws = scales(70, 11), scales(140, 12)
