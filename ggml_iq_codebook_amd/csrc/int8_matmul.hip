@@ -217,7 +217,7 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* row, int at, int depth
 template <int kDepth>
 __device__ __forceinline__ int swizzle(int row)
 {
-    return kDepth == 64 ? (row >> 1) & 3 : row & 7;
+    return kDepth == 64 ? (row >> 1) & 3 : row & (kDepth / 16 - 1);
 }
 
 // Waits until at most kLeft of this wave's loads are under way and all its LDS
