@@ -71,21 +71,31 @@ def _refuse(t, name, index):
     raise ValueError("%s must be on cuda:%d" % (name, index))
 
 
-def _matrix(t, name, index, dtype=None):
-    """A two-dimensional tensor on that GPU with consecutive values in a row; its row stride."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        _refuse(t, name, index)
+def _row_stride(t, name, dtype):
+    """The row stride of a two-dimensional tensor with consecutive values in a row."""
     if dtype is None:
         if t.dtype not in _DTYPES:
             raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
     elif t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 2:
+    stride = t.stride()
+    if len(stride) != 2:
         raise ValueError("%s must have two dimensions" % name)
-    stride, step = t.stride()
-    if step != 1 and t.shape[1] != 1:
+    if stride[1] != 1 and t.shape[1] != 1:
         raise ValueError("%s must have consecutive values in a row" % name)
-    return stride
+    return stride[0]
+
+
+def _first(t, name, dtype=None):
+    """A call's first matrix: the GPU it is on, and its row stride."""
+    return _on_gpu(t, name), _row_stride(t, name, dtype)
+
+
+def _matrix(t, name, index, dtype=None):
+    """A further matrix, on that GPU: its row stride."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _refuse(t, name, index)
+    return _row_stride(t, name, dtype)
 
 
 def _vector(t, dtype, shape, name, index):
@@ -104,9 +114,14 @@ def _vector(t, dtype, shape, name, index):
 _stream = torch._C._cuda_getCurrentRawStream
 
 
-def _output(out, rows, cols, dtype, index, name):
+def _output(out, rows, cols, like, index, name):
+    """The result of a call, a matrix like the tensor `like` or of the type it
+    is, and its row stride."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=_DEVICES[index]), cols
+        if isinstance(like, torch.Tensor):
+            return like.new_empty((rows, cols)), cols
+        return torch.empty((rows, cols), dtype=like, device=_DEVICES[index]), cols
+    dtype = like.dtype if isinstance(like, torch.Tensor) else like
     stride = _matrix(out, name, index, dtype)
     if out.shape != (rows, cols):
         raise ValueError("%s must be [%d, %d]" % (name, rows, cols))
@@ -133,8 +148,7 @@ def quantize_rows(x, *, status=None, check=True):
     makes the weight of the products below.  A row with a NaN or an infinity is
     reported (IQ_ERR_NONFINITE) and written as zeros.
     """
-    index = _on_gpu(x, "x")
-    ldx = _matrix(x, "x", index)
+    index, ldx = _first(x, "x")
     rows, cols = x.shape
     word, status = _status(status, check, index)
     device = _DEVICES[index]
@@ -156,8 +170,8 @@ def int8_matmul(x, x_scale, w, w_scale, *, dtype=torch.bfloat16, out=None):
     ``quantize_rows`` gives them).  The sums are exact.  Returns
     [tokens, channels] in ``dtype`` (or in the type of ``out``).
     """
-    index = _on_gpu(x, "x")
-    ldx, ldw = _matrix(x, "x", index, torch.int8), _matrix(w, "w", index, torch.int8)
+    index, ldx = _first(x, "x", torch.int8)
+    ldw = _matrix(w, "w", index, torch.int8)
     tokens, depth = x.shape
     channels, w_depth = w.shape
     if w_depth != depth:
@@ -183,15 +197,14 @@ def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
     has its type.  A token with a NaN or an infinity is reported
     (IQ_ERR_NONFINITE) and answered with zeros.
     """
-    index = _on_gpu(x, "x")
-    ldx, ldw = _matrix(x, "x", index), _matrix(w, "w", index, torch.int8)
+    index, ldx = _first(x, "x")
+    ldw = _matrix(w, "w", index, torch.int8)
     tokens, depth = x.shape
     channels, w_depth = w.shape
     if w_depth != depth:
         raise ValueError("w must be [channels, %d]" % depth)
     ws = _vector(w_scale, torch.float32, (channels,), "w_scale", index)
-    dtype = x.dtype
-    y, ldy = _output(out, tokens, channels, dtype, index, "out")
+    y, ldy = _output(out, tokens, channels, x, index, "out")
     word, status = _status(status, check, index)
     L = iq.load()
     need, work, space = L.iq_int8_linear_workspace(tokens, depth), None, None
@@ -199,7 +212,7 @@ def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
         work = torch.empty((need,), dtype=torch.uint8, device=_DEVICES[index])
         space = work.data_ptr()
     code = L.iq_int8_linear(
-        _DTYPES[dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, ws, tokens, channels, depth,
+        _DTYPES[x.dtype], x.data_ptr(), ldx, w.data_ptr(), ldw, ws, tokens, channels, depth,
         y.data_ptr(), ldy, space, need, word, _stream(index))
     iq._check(code, "iq_int8_linear")
     iq._raise_on_status(status, check, "iq_int8_linear")
@@ -217,8 +230,7 @@ def int8_expert_matmul(x, x_scale, w, w_scale, offsets, order=None, *, top_k=1,
     ``order`` it is row p of ``x`` (already dispatched).  Rows of dropped
     choices are zeros.
     """
-    index = _on_gpu(x, "x")
-    ldx = _matrix(x, "x", index, torch.int8)
+    index, ldx = _first(x, "x", torch.int8)
     tokens, depth = x.shape
     if not isinstance(w, torch.Tensor) or w.get_device() != index:
         _refuse(w, "w", index)
@@ -303,23 +315,21 @@ def _route(position, offsets, index):
     return tokens, top_k, experts, places, ends
 
 
-def _sorted(t, name, rows, index):
-    ld = _matrix(t, name, index)
+def _has_rows(t, name, rows):
     if t.shape[0] != rows:
         raise ValueError("%s must have %d rows" % (name, rows))
-    return ld
 
 
 def expert_dispatch(x, position, offsets, *, out=None):
     """Tokens copied to the places of their choices: [tokens * top_k, width],
     row position[t, j] holding ``x[t]`` (zeros where the choice was dropped)."""
-    index = _on_gpu(x, "x")
+    index, ldx = _first(x, "x")
     tokens, top_k, experts, places, ends = _route(position, offsets, index)
-    ldx = _sorted(x, "x", tokens, index)
-    width, dtype = x.shape[1], x.dtype
-    out, ldo = _output(out, tokens * top_k, width, dtype, index, "out")
+    _has_rows(x, "x", tokens)
+    width = x.shape[1]
+    out, ldo = _output(out, tokens * top_k, width, x, index, "out")
     code = iq.load().iq_expert_dispatch(
-        _DTYPES[dtype], x.data_ptr(), ldx, tokens, width, places, top_k, ends, experts,
+        _DTYPES[x.dtype], x.data_ptr(), ldx, tokens, width, places, top_k, ends, experts,
         out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_dispatch")
     return out
@@ -328,13 +338,13 @@ def expert_dispatch(x, position, offsets, *, out=None):
 def expert_dispatch_backward(grad, position, offsets, *, out=None):
     """The gradient of ``expert_dispatch``: for the gradient of its result, that
     of ``x``, the sum over each token's kept choices."""
-    index = _on_gpu(grad, "grad")
+    index, ldg = _first(grad, "grad")
     tokens, top_k, experts, places, ends = _route(position, offsets, index)
-    ldg = _sorted(grad, "grad", tokens * top_k, index)
-    width, dtype = grad.shape[1], grad.dtype
-    out, ldo = _output(out, tokens, width, dtype, index, "out")
+    _has_rows(grad, "grad", tokens * top_k)
+    width = grad.shape[1]
+    out, ldo = _output(out, tokens, width, grad, index, "out")
     code = iq.load().iq_expert_dispatch_backward(
-        _DTYPES[dtype], grad.data_ptr(), ldg, tokens, width, places, top_k, ends, experts,
+        _DTYPES[grad.dtype], grad.data_ptr(), ldg, tokens, width, places, top_k, ends, experts,
         out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_dispatch_backward")
     return out
@@ -343,14 +353,14 @@ def expert_dispatch_backward(grad, position, offsets, *, out=None):
 def expert_combine(y, position, offsets, weights, *, out=None):
     """Rows brought back to their tokens: out[t] = the sum over the kept choices
     j of weights[t, j] * y[position[t, j]] (``weights`` fp32 [tokens, top_k])."""
-    index = _on_gpu(y, "y")
+    index, ldy = _first(y, "y")
     tokens, top_k, experts, places, ends = _route(position, offsets, index)
-    ldy = _sorted(y, "y", tokens * top_k, index)
-    width, dtype = y.shape[1], y.dtype
+    _has_rows(y, "y", tokens * top_k)
+    width = y.shape[1]
     factors = _vector(weights, torch.float32, position.shape, "weights", index)
-    out, ldo = _output(out, tokens, width, dtype, index, "out")
+    out, ldo = _output(out, tokens, width, y, index, "out")
     code = iq.load().iq_expert_combine(
-        _DTYPES[dtype], y.data_ptr(), ldy, tokens, width, places, top_k, ends, experts, factors,
+        _DTYPES[y.dtype], y.data_ptr(), ldy, tokens, width, places, top_k, ends, experts, factors,
         out.data_ptr(), ldo, _stream(index))
     iq._check(code, "iq_expert_combine")
     return out
@@ -359,16 +369,16 @@ def expert_combine(y, position, offsets, weights, *, out=None):
 def expert_combine_backward(grad, y, position, offsets, weights):
     """The gradients of ``expert_combine`` for the gradient ``grad`` [tokens,
     width] of its result: (that of ``y``, that of ``weights``)."""
-    index = _on_gpu(y, "y")
+    index, ldy = _first(y, "y")
     tokens, top_k, experts, places, ends = _route(position, offsets, index)
-    ldy = _sorted(y, "y", tokens * top_k, index)
+    _has_rows(y, "y", tokens * top_k)
     width, dtype = y.shape[1], y.dtype
     ldo = _matrix(grad, "grad", index, dtype)
     if grad.shape != (tokens, width):
         raise ValueError("grad must be [%d, %d]" % (tokens, width))
     factors = _vector(weights, torch.float32, position.shape, "weights", index)
-    y_grad = torch.empty((tokens * top_k, width), dtype=dtype, device=_DEVICES[index])
-    weights_grad = torch.empty((tokens, top_k), dtype=torch.float32, device=_DEVICES[index])
+    y_grad = y.new_empty((tokens * top_k, width))
+    weights_grad = weights.new_empty((tokens, top_k))
     code = iq.load().iq_expert_combine_backward(
         _DTYPES[dtype], grad.data_ptr(), ldo, y.data_ptr(), ldy, tokens, width, places, top_k,
         ends, experts, factors, y_grad.data_ptr(), width, weights_grad.data_ptr(), _stream(index))
