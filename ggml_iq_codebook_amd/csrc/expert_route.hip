@@ -7,10 +7,15 @@
 // count as one more expert behind the last, so `position` is a permutation of
 // all choices and every row of a sorted tensor has exactly one writer.
 //
+// Bound by latency: 1024 choices of 16 experts 3.7 us, 32768 of 64 experts 8.7 us
+// in two launches.
+//
 // The copies are bound by HBM.  They go token by token: a token's row is read
 // once for all its choices (dispatch), or its choices' rows are read and
 // summed in registers (combine), 16 bytes a lane, with no intermediate tensor
-// and no atomics.
+// and no atomics.  4096 tokens of 4096 bf16 values with 8 choices each: dispatch
+// 52 us (5.8 TB/s), combine 56 us and the gradient of dispatch 55 us (5.4 TB/s),
+// the gradients of combine 110 us (5.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "iq_layers.h"

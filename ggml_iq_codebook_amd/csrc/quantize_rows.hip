@@ -3,7 +3,10 @@
 // reciprocal and the product rounded to nearest, the division correctly rounded.
 //
 // Bound by HBM: a row is read once, kept in registers while its maximum is
-// found, and written as one byte per value.
+// found, and written as one byte per value.  16384 bf16 rows of 4096: 38 us,
+// 5.3 TB/s read and written together (a large copy: 5.1); 4096 rows: 11.5 us.
+// A correctly rounded division for each value, in place of the reciprocal and
+// its check, took 19 us for these 4096 rows.
 #include <hip/hip_runtime.h>
 
 #include "layers_launch.hpp"
