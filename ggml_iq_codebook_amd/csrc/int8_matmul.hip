@@ -10,6 +10,7 @@
 // channels of one token and go out as one store.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "iq_layers.h"
@@ -229,9 +230,11 @@ __device__ __forceinline__ void wait_and_meet()
 }
 
 // kWT x kWC waves share a tile of kRows rows of y by kChannels channels, each
-// a part of kRows/kWT by kChannels/kWC, in steps of kDepth of the depth.  The
-// tiles of both operands go through a ring of buffers in LDS; what the depth
-// leaves beyond whole steps has a buffer of its own, filled at the start.
+// a part of kRows/kWT by kChannels/kWC, in steps of kDepth of the depth.  On the
+// two smallest tiles kWK waves share a part, each on its share of every step, and
+// add their sums at the end.  The tiles of both operands go through a ring of
+// buffers in LDS; what the depth leaves beyond whole steps has a buffer of its
+// own, filled at the start.
 //
 // kDirect: rows start on 16 bytes, and pieces are copied straight into LDS,
 // kStages - 1 steps ahead.  Otherwise they pass through registers, four steps
@@ -254,12 +257,12 @@ __device__ __forceinline__ void wait_and_meet()
 // against 74; v_mfma_i32_32x32x32_i8 in its place: 71.
 // Small tiles are bound by the latency of their first loads, products by expert
 // of few rows by HBM (16 tokens, 2 of 16 experts of 1536 x 4096: 18 us, 5.5 TB/s).
-template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,
-          bool kDirect, bool kExperts>
-__global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kernel(Int8Product p,
-                                                                                 int channel_tiles)
+template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int kStages,
+          bool kPingPong, bool kDirect, bool kExperts>
+__global__ __launch_bounds__(kWT* kWC* kWK* kWave, kWT* kWC* kWK / 4) void int8_tile_kernel(
+    Int8Product p, int channel_tiles)
 {
-    constexpr int kWaves = kWT * kWC, kThreads = kWaves * kWave;
+    constexpr int kWaves = kWT * kWC * kWK, kThreads = kWaves * kWave;
     constexpr int kFT = kRows / kWT / 16, kFC = kChannels / kWC / 16;
     constexpr int kPieces = kDepth / 16;
     constexpr int kRowsPerLoad = kWave / kPieces;
@@ -310,13 +313,15 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
     };
 
     v4i acc[kFC][kFT] = {};
-    const int wt = wave % kWT, wc = wave / kWT;
+    const int wt = wave % kWT, wc = wave / kWT % kWC, wk = wave / (kWT * kWC);
     const int quarter = lane / 16;
     const int row_c = wc * kFC * 16 + lane % 16;
     const int row_t = kChannels + wt * kFT * 16 + lane % 16;
-    constexpr int kParts = kDepth / 64;
+    // A step's parts of 64 that are this wave's: wk, wk + kWK, ...
+    constexpr int kParts = kDepth / 64 / kWK;
+    static_assert(kParts > 0 && (kWK == 1 || kFC == 1), "waves that share a part");
     auto read = [&](int b, int k, v4i (&a)[kFC], v4i (&x)[kFT]) {
-        const int piece = 4 * k + quarter;
+        const int piece = 4 * (kWK * k + wk) + quarter;
 #pragma unroll
         for (int i = 0; i < kFC; ++i)
             a[i] = *reinterpret_cast<const v4i*>(
@@ -447,6 +452,21 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
         }
     }
 
+    if constexpr (kWK > 1) {
+        wait_and_meet<0>();
+        v4i* sums = reinterpret_cast<v4i*>(&staged[0][0]) + (wave % (kWT * kWC)) * kFT * kWave + lane;
+        constexpr int kNext = kWT * kWC * kFT * kWave;
+        if (wk) {
+#pragma unroll
+            for (int j = 0; j < kFT; ++j) sums[(wk - 1) * kNext + j * kWave] = acc[0][j];
+        }
+        wait_and_meet<0>();
+        if (wk) return;
+#pragma unroll
+        for (int k = 0; k < kWK - 1; ++k)
+#pragma unroll
+            for (int j = 0; j < kFT; ++j) acc[0][j] += sums[k * kNext + j * kWave];
+    }
     const int wave_channel = channel0 + wc * kFC * 16;
     const float* sw = p.w_scale + (int64_t)t.expert * p.channels;
     float scale[kFC][4];
@@ -522,39 +542,42 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void int8_tile_kerne
         write(Int<IQ_DTYPE_F32>());
 }
 
-template <int kRows, int kChannels, int kWT, int kWC, int kDepth, int kStages, bool kPingPong,
-          bool kDirect>
+// Every expert (and the dropped rows) may end in a tile that is not full.
+int64_t workgroups(const Int8Product& p, int rows, int channel_tiles)
+{
+    const int64_t row_tiles = p.experts ? std::min(p.rows, p.rows / rows + p.experts + 1)
+                                        : (p.rows + rows - 1) / rows;
+    return row_tiles * channel_tiles;
+}
+
+template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int kStages,
+          bool kPingPong, bool kDirect>
 hipError_t launch_tiles(const Int8Product& p, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
-    // Every expert (and the dropped rows) may end in a tile that is not full.
-    const int64_t row_tiles = p.experts ? min(p.rows, p.rows / kRows + p.experts + 1)
-                                        : (p.rows + kRows - 1) / kRows;
-    const int64_t wgs = row_tiles * channel_tiles;
+    const int64_t wgs = workgroups(p, kRows, channel_tiles);
     if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)wgs), threads(kWT * kWC * kWave);
+    const dim3 grid((unsigned)wgs), threads(kWT * kWC * kWK * kWave);
     if (p.experts)
-        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kDepth, kStages,
+        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
                                              kPingPong, kDirect, true>),
                            grid, threads, 0, stream, p, channel_tiles);
     else
-        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kDepth, kStages,
+        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
                                              kPingPong, kDirect, false>),
                            grid, threads, 0, stream, p, channel_tiles);
     return hipGetLastError();
 }
 
-// The expected time of a tile size in microseconds.  Compute units take their
-// tiles one after another, each costing `start` for its first loads and its
-// results, and `depth` for every 1024 of the depth, plus `full` of that in the
-// measure in which all units are busy (the matrix cores then share the card's
-// power).  Of the small tiles two fit a unit's LDS at once: each pair costs
-// `start` and `depth`, a single one `start1` and `depth1`.  `once` is what the
-// whole product costs beside them.
+// The expected time of a tile size in microseconds: `once` for the product, and
+// for each tile that a compute unit takes in turn `start` (its first loads and
+// its results) and `depth` for every 1024 of the depth.  Where not all units are
+// busy to the end those that are go faster, the small tiles because they share
+// L2 and LDS, the large ones the card's power: `start_full` and `depth_full`
+// count with the tiles a unit has on average, not the most that one has.
 struct TileTime {
     int rows, channels;
-    bool pairs;
-    double once, start, depth, full, start1, depth1;
+    double once, start, depth, start_full, depth_full;
 };
 
 double expected_time(const Int8Product& p, int cus, const TileTime& t)
@@ -567,41 +590,42 @@ double expected_time(const Int8Product& p, int cus, const TileTime& t)
         const double used = p.experts * (1.0 - exp(-each));
         row_tiles = fmax(used, (double)p.rows / t.rows + 0.5 * used);
     }
-    const double tiles = row_tiles * ((p.channels + t.channels - 1) / t.channels);
-    const double each = ceil(tiles / cus), k = p.depth / 1024.0;
-    if (t.pairs) {
-        const double pairs = floor(0.5 * each), single = each - 2.0 * pairs;
-        return t.once + pairs * (t.start + t.depth * k) + single * (t.start1 + t.depth1 * k);
-    }
-    return t.once + each * (t.start + t.depth * k) + t.full * k * tiles / cus;
+    const double average = row_tiles * ((p.channels + t.channels - 1) / t.channels) / cus;
+    const double k = p.depth / 1024.0;
+    return t.once + ceil(average) * (t.start + t.depth * k) +
+           average * (t.start_full + t.depth_full * k);
 }
 
-// Fitted to the times of every tile in 240 products of 1 to 4096 tokens, 256 to
+// Fitted to the times of every tile in 510 products of 1 to 4096 tokens, 256 to
 // 5632 channels and depths of 512 to 5632.  The tile with the least expected
-// time took 1 % longer than the fastest of ten sizes on average (128 x 128
-// alone: 30 %).
+// time took 0.4 % longer than the fastest on average, 33 % at worst (128 x 128
+// alone: 30 % on average).
 constexpr TileTime kDense[] = {
-    {32, 32, true, 3.1, 1.40, 1.27, 0.0, 0.0, 1.28},
-    {64, 64, true, 3.3, 2.36, 2.65, 0.0, 2.80, 1.47},
-    {64, 128, false, 2.1, 3.38, 1.88, 0.52, 0.0, 0.0},
-    {128, 128, false, 1.4, 4.58, 2.63, 1.03, 0.0, 0.0},
-    {128, 256, false, 0.0, 5.67, 5.12, 3.89, 0.0, 0.0},
-    {256, 256, false, 0.0, 9.77, 6.87, 7.01, 0.0, 0.0}};
+    {16, 16, 3.11, 0.03, 0.34, 0.14, 0.0},
+    {32, 32, 3.09, 0.18, 0.72, 0.42, 0.0},
+    {64, 64, 1.97, 2.17, 1.31, 0.82, 0.34},
+    {64, 128, 2.05, 2.11, 2.36, 1.53, 0.32},
+    {128, 128, 2.16, 2.84, 3.04, 2.35, 0.79},
+    {128, 256, 2.28, 3.41, 5.54, 4.76, 2.11},
+    {256, 256, 5.22, 6.53, 6.31, 5.15, 5.52}};
 // Likewise for products by expert, 1 to 4096 tokens of 2 and 8 choices, 8, 16
-// and 64 experts, chosen evenly and not: 4 % longer than the fastest.  A tile
-// starts later than in a dense product, its weight coming from HBM.
+// and 64 experts, chosen evenly and not: 3 % longer than the fastest.  Tiles take
+// longer than in a dense product, their weight coming from HBM.
 constexpr TileTime kByExpert[] = {
-    {32, 32, true, 4.6, 4.29, 1.29, 0.0, 0.49, 1.81},
-    {64, 64, true, 4.1, 5.77, 2.79, 0.0, 3.93, 1.42},
-    {128, 128, false, 3.1, 6.67, 1.09, 2.94, 0.0, 0.0},
-    {128, 256, false, 1.1, 7.80, 3.39, 6.01, 0.0, 0.0},
-    {256, 256, false, 0.6, 10.38, 5.70, 6.83, 0.0, 0.0}};
-// And where rows do not start on 16 bytes: 1 % longer than the fastest.
+    {16, 16, 4.46, 0.0, 0.46, 0.59, 0.0},
+    {32, 32, 4.43, 0.0, 0.70, 1.29, 0.27},
+    {64, 64, 3.21, 1.36, 1.43, 3.01, 0.77},
+    {64, 128, 4.36, 0.19, 2.20, 4.90, 1.13},
+    {128, 128, 3.95, 1.37, 2.75, 5.68, 1.51},
+    {128, 256, 4.54, 1.38, 5.03, 7.46, 3.72},
+    {256, 256, 5.39, 6.53, 6.02, 5.40, 5.65}};
+// And where rows do not start on 16 bytes: 2 % longer than the fastest.
 constexpr TileTime kUnaligned[] = {
-    {32, 32, true, 6.7, 2.88, 2.19, 0.0, 0.70, 2.08},
-    {64, 64, true, 2.7, 8.51, 4.96, 0.0, 5.90, 2.84},
-    {128, 128, false, 1.3, 10.82, 5.18, 1.52, 0.0, 0.0},
-    {128, 256, false, 0.0, 13.0, 12.5, 2.5, 0.0, 0.0}};
+    {16, 16, 7.38, 0.34, 0.84, 0.46, 0.0},
+    {32, 32, 7.09, 2.27, 1.74, 0.0, 0.0},
+    {64, 64, 7.37, 2.78, 3.30, 0.41, 0.0},
+    {128, 128, 2.94, 9.96, 6.87, 2.17, 0.0},
+    {128, 256, 2.95, 9.78, 14.62, 4.83, 0.0}};
 
 // The rows and channels of the entry with the least expected time.
 template <int kN>
@@ -630,19 +654,21 @@ hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream
                         reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
     if (!direct) {
         switch (choose_tile(p, cus, kUnaligned)) {
-        case 32032: return launch_tiles<32, 32, 2, 2, 128, 2, false, false>(p, stream);
-        case 64064: return launch_tiles<64, 64, 4, 2, 128, 2, false, false>(p, stream);
-        case 128128: return launch_tiles<128, 128, 4, 4, 128, 2, false, false>(p, stream);
-        default: return launch_tiles<128, 256, 2, 4, 64, 2, false, false>(p, stream);
+        case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 2, false, false>(p, stream);
+        case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 2, false, false>(p, stream);
+        case 64064: return launch_tiles<64, 64, 4, 2, 1, 128, 2, false, false>(p, stream);
+        case 128128: return launch_tiles<128, 128, 4, 4, 1, 128, 2, false, false>(p, stream);
+        default: return launch_tiles<128, 256, 2, 4, 1, 64, 2, false, false>(p, stream);
         }
     }
     switch (p.experts ? choose_tile(p, cus, kByExpert) : choose_tile(p, cus, kDense)) {
-    case 32032: return launch_tiles<32, 32, 2, 2, 256, 4, false, true>(p, stream);
-    case 64064: return launch_tiles<64, 64, 2, 2, 128, 4, false, true>(p, stream);
-    case 64128: return launch_tiles<64, 128, 2, 4, 128, 4, true, true>(p, stream);
-    case 128128: return launch_tiles<128, 128, 4, 2, 128, 4, true, true>(p, stream);
-    case 128256: return launch_tiles<128, 256, 2, 4, 64, 4, true, true>(p, stream);
-    default: return launch_tiles<256, 256, 4, 2, 64, 4, true, true>(p, stream);
+    case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 4, false, true>(p, stream);
+    case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 4, false, true>(p, stream);
+    case 64064: return launch_tiles<64, 64, 4, 2, 1, 256, 4, true, true>(p, stream);
+    case 64128: return launch_tiles<64, 128, 2, 4, 1, 128, 4, true, true>(p, stream);
+    case 128128: return launch_tiles<128, 128, 4, 2, 1, 128, 4, true, true>(p, stream);
+    case 128256: return launch_tiles<128, 256, 2, 4, 1, 64, 4, true, true>(p, stream);
+    default: return launch_tiles<256, 256, 4, 2, 1, 64, 4, true, true>(p, stream);
     }
 }
 
