@@ -596,29 +596,37 @@ double expected_time(const Int8Product& p, int cus, const TileTime& t)
            average * (t.start_full + t.depth_full * k);
 }
 
-// Fitted to the times of every tile in 510 products of 1 to 4096 tokens, 256 to
+// Fitted to the times of every tile in 700 products of 1 to 4096 tokens, 256 to
 // 5632 channels and depths of 512 to 5632.  The tile with the least expected
-// time took 0.4 % longer than the fastest on average, 33 % at worst (128 x 128
-// alone: 30 % on average).
+// time took 0.2 % longer than the fastest on average, 7 % at worst; without the
+// four sizes with a side of 192 1.5 % and 38 %, 128 x 128 alone 77 %.
 constexpr TileTime kDense[] = {
-    {16, 16, 3.11, 0.03, 0.34, 0.14, 0.0},
-    {32, 32, 3.09, 0.18, 0.72, 0.42, 0.0},
-    {64, 64, 1.97, 2.17, 1.31, 0.82, 0.34},
-    {64, 128, 2.05, 2.11, 2.36, 1.53, 0.32},
-    {128, 128, 2.16, 2.84, 3.04, 2.35, 0.79},
-    {128, 256, 2.28, 3.41, 5.54, 4.76, 2.11},
-    {256, 256, 5.22, 6.53, 6.31, 5.15, 5.52}};
+    {16, 16, 3.10, 0.06, 0.34, 0.10, 0.0},
+    {32, 32, 3.08, 0.22, 0.71, 0.39, 0.0},
+    {64, 64, 2.11, 2.04, 1.33, 0.93, 0.26},
+    {64, 128, 2.29, 1.86, 2.43, 1.80, 0.05},
+    {64, 192, 2.52, 2.44, 3.23, 2.06, 0.11},
+    {128, 128, 2.66, 2.39, 3.14, 2.45, 0.39},
+    {128, 192, 2.87, 3.81, 4.16, 2.63, 0.53},
+    {192, 128, 2.73, 3.28, 3.93, 2.76, 0.70},
+    {128, 256, 2.79, 3.13, 5.56, 4.49, 1.71},
+    {192, 192, 3.49, 4.42, 5.03, 3.57, 2.50},
+    {256, 256, 3.42, 8.79, 5.83, 4.41, 5.17}};
 // Likewise for products by expert, 1 to 4096 tokens of 2 and 8 choices, 8, 16
 // and 64 experts, chosen evenly and not: 3 % longer than the fastest.  Tiles take
 // longer than in a dense product, their weight coming from HBM.
 constexpr TileTime kByExpert[] = {
-    {16, 16, 4.46, 0.0, 0.46, 0.59, 0.0},
-    {32, 32, 4.43, 0.0, 0.70, 1.29, 0.27},
-    {64, 64, 3.21, 1.36, 1.43, 3.01, 0.77},
-    {64, 128, 4.36, 0.19, 2.20, 4.90, 1.13},
-    {128, 128, 3.95, 1.37, 2.75, 5.68, 1.51},
-    {128, 256, 4.54, 1.38, 5.03, 7.46, 3.72},
-    {256, 256, 5.39, 6.53, 6.02, 5.40, 5.65}};
+    {16, 16, 4.26, 0.0, 0.46, 0.61, 0.0},
+    {32, 32, 4.14, 0.0, 0.78, 1.35, 0.20},
+    {64, 64, 2.89, 1.81, 1.41, 2.73, 0.75},
+    {64, 128, 4.44, 0.0, 2.25, 5.29, 0.75},
+    {64, 192, 5.12, 0.05, 3.24, 6.65, 0.53},
+    {128, 128, 4.98, 0.0, 2.79, 6.54, 1.07},
+    {128, 192, 3.11, 3.45, 4.33, 5.62, 0.97},
+    {192, 128, 3.33, 2.96, 3.62, 4.81, 1.62},
+    {128, 256, 5.08, 0.65, 5.31, 7.97, 2.93},
+    {192, 192, 1.43, 6.58, 4.15, 3.36, 3.72},
+    {256, 256, 8.13, 3.32, 5.92, 6.39, 5.38}};
 // And where rows do not start on 16 bytes: 2 % longer than the fastest.
 constexpr TileTime kUnaligned[] = {
     {16, 16, 7.38, 0.34, 0.84, 0.46, 0.0},
@@ -666,7 +674,11 @@ hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream
     case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 4, false, true>(p, stream);
     case 64064: return launch_tiles<64, 64, 4, 2, 1, 256, 4, true, true>(p, stream);
     case 64128: return launch_tiles<64, 128, 2, 4, 1, 128, 4, true, true>(p, stream);
+    case 64192: return launch_tiles<64, 192, 4, 2, 1, 128, 4, true, true>(p, stream);
     case 128128: return launch_tiles<128, 128, 4, 2, 1, 128, 4, true, true>(p, stream);
+    case 128192: return launch_tiles<128, 192, 4, 2, 1, 128, 3, true, true>(p, stream);
+    case 192128: return launch_tiles<192, 128, 4, 2, 1, 128, 3, true, true>(p, stream);
+    case 192192: return launch_tiles<192, 192, 4, 2, 1, 64, 4, true, true>(p, stream);
     case 128256: return launch_tiles<128, 256, 2, 4, 1, 64, 4, true, true>(p, stream);
     default: return launch_tiles<256, 256, 4, 2, 1, 64, 4, true, true>(p, stream);
     }
