@@ -37,6 +37,10 @@ struct Value<IQ_DTYPE_F16> {
     }
     __device__ __forceinline__ static raw store(float f)
     {
+        // Keeps a product from being rounded to fp16 in one step with its
+        // conversion (v_fma_mixlo_f16), which the compiler does in some kernels
+        // and not in others: every result is rounded to fp32 first.
+        asm("" : "+v"(f));
         return __builtin_bit_cast(uint16_t, (_Float16)f);
     }
 };
