@@ -130,10 +130,10 @@ iq_status_t iq_int8_matmul(const int8_t* x, int64_t ldx, const float* x_scale, c
     return from_hip(iqk::launch_int8_product(p, cus, stream));
 }
 
-int64_t iq_int8_linear_workspace(int64_t tokens, int64_t depth)
+int64_t iq_int8_linear_workspace(int64_t tokens, int64_t channels, int64_t depth)
 {
-    if (tokens < 1 || tokens > INT32_MAX || depth < 1 || depth > IQ_MAX_INT8_DEPTH ||
-        iqk::int8_decode_takes(tokens, depth))
+    if (tokens < 1 || tokens > INT32_MAX || channels < 1 || channels > INT32_MAX || depth < 1 ||
+        depth > IQ_MAX_INT8_DEPTH || iqk::int8_decode_takes(tokens, channels, depth))
         return 0;
     return tokens * code_stride(depth) + round_up(tokens * 4, 16);
 }
@@ -144,7 +144,7 @@ iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const i
                            int64_t workspace_bytes, int32_t* status, hipStream_t stream)
 {
     if (bad_product(tokens, channels, depth, ldx, ldw, ldy, tokens)) return IQ_ERR_SHAPE;
-    const int64_t need = iq_int8_linear_workspace(tokens, depth);
+    const int64_t need = iq_int8_linear_workspace(tokens, channels, depth);
     if (tokens && (!x || !w || !w_scale || !y || (need && !workspace))) return IQ_ERR_NULL;
     const int bytes = value_bytes(dtype);
     if (!bytes || !aligned(x, bytes) || !aligned(y, bytes) || !aligned(w_scale, 4) ||
@@ -162,7 +162,7 @@ iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const i
                                 tokens, (int)channels,   (int)depth, (int)dtype,
                                 nullptr, nullptr, 0,     1};
     return run_with_status(status, stream, [&](int32_t* s) {
-        if (iqk::int8_decode_takes(tokens, depth))
+        if (iqk::int8_decode_takes(tokens, channels, depth))
             return iqk::launch_int8_decode(p, dtype, x, ldx, s, stream);
         const hipError_t e = iqk::launch_quantize_rows(dtype, x, ldx, tokens, depth, codes, ldc,
                                                        scale, s, stream);

@@ -311,7 +311,7 @@ PyObject* int8_linear(PyObject* const* a)
     const float* ws = array<float>(c, a[2], "w_scale", at::kFloat, {w.rows});
     const Result y(c, a[3], x.rows, w.rows, x.t.scalar_type());
     int32_t* status = status_word(c, a[4]);
-    const int64_t need = iq_int8_linear_workspace(x.rows, x.cols);
+    const int64_t need = iq_int8_linear_workspace(x.rows, w.rows, x.cols);
     at::Tensor work;
     if (need) work = at::empty({need}, c.options(at::kByte));
     check(unlocked([&] {

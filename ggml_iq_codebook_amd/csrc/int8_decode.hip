@@ -10,9 +10,11 @@
 // of 64 bytes a row under way at once.  The 8 partial sums are integers, so
 // adding them in LDS is exact.
 //
-// One token through 4096 x 4096: 6.2 us of GPU time, as two launches 3.5 + 6.9;
-// as a user calls it, back to back, 8.8 and 13.5 us (16.8 MB of weight at the
-// rate of a large copy: 3.3 us).
+// One token through 4096 x 4096: 7.6 us in a graph with its weight in HBM, as two
+// launches 10.0; called back to back on a weight that stays in the caches 6.2 us
+// (16.8 MB at the rate of a large copy: 3.3 us).  32 or 64 channels to a
+// workgroup, which halve the rounding of wide weights, took 9.4 and 14.0 us here
+// and no less than two launches on 32768 channels.
 #include <hip/hip_runtime.h>
 
 #include "layers_launch.hpp"
@@ -26,7 +28,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kTokens = 16;           // columns of the matrix instruction
-constexpr int kChannels = 16;         // and its rows
+constexpr int kChannels = kDecodeChannels;   // and its rows
 constexpr int kFlight = 8;            // pieces of the weight under way
 constexpr int kPart = kWave * kChunk; // values a wave rounds at once
 constexpr int kKeep = kDecodeParts / kWaves;

@@ -37,17 +37,32 @@ struct Int8Product {
 
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream);
 
-// The layer for a few tokens, rounding included, as one launch.  Its tokens are
-// dealt out in parts of 512 values of which a workgroup keeps kDecodeParts.
+// The layer for a few tokens, rounding included, as one launch.  A workgroup has
+// 16 channels and rounds all tokens, dealt out in parts of 512 values of which it
+// keeps up to kDecodeParts.
 constexpr int kDecodeParts = 32;
+constexpr int kDecodeChannels = 16;
 __host__ __device__ constexpr int decode_stride(int depth)
 {
     // Whole pieces of 64, and rows that start on different banks.
     return (depth + 63) / 64 * 64 + 16;
 }
-inline bool int8_decode_takes(int64_t tokens, int64_t depth)
+// Where one launch pays: its rounding is repeated by every workgroup, so its cost
+// goes with the parts and with the rounds of workgroups on the 256 compute
+// units.  GPU time, one launch against two, us (as calls of their own the second
+// launch adds 3 more):
+//   channels x depth, tokens   1            2            4            8
+//   1024 x 1024                4.3 / 6.0    4.6 / 6.2    4.8 / 6.2    5.9 / 6.4
+//   4096 x 4096                7.6 / 10.0   8.5 / 9.8   10.5 / 9.9
+//   5632 x 2048                7.2 / 7.8    7.8 / 7.9    9.3 / 8.0
+//   4096 x 16384              19.2 / 25.5
+//   16384 x 4096              17.7 / 19.7  19.0 / 18.9  21.5 / 19.2
+//   32768 x 2048              21.3 / 18.7
+inline bool int8_decode_takes(int64_t tokens, int64_t channels, int64_t depth)
 {
-    return tokens <= 16 && tokens * ((depth + 511) / 512) <= kDecodeParts;
+    const int64_t rounds = (channels + 256 * kDecodeChannels - 1) / (256 * kDecodeChannels);
+    return tokens <= 16 && rounds <= 4 &&
+           tokens * ((depth + 511) / 512) * rounds <= (tokens == 1 ? kDecodeParts : kDecodeParts / 2);
 }
 // p.x, p.x_scale are not used; y has the type of x.
 hipError_t launch_int8_decode(const Int8Product& p, int dtype, const void* x, int64_t ldx,

@@ -59,7 +59,7 @@ def declare(L):
     }.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, c
-    for name, args in {"iq_int8_linear_workspace": [i64, i64],
+    for name, args in {"iq_int8_linear_workspace": [i64, i64, i64],
                        "iq_expert_sort_workspace": [i64, i32]}.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, i64

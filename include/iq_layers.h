@@ -54,9 +54,9 @@ iq_status_t iq_int8_matmul(const int8_t* x, int64_t ldx, const float* x_scale, c
 
 /* iq_quantize_rows of x followed by iq_int8_matmul: a served layer on
  * activations as they come.  y has the type of x.  `workspace` holds the codes
- * and scales between the two, iq_int8_linear_workspace(tokens, depth) bytes,
- * 16-byte aligned; it may be NULL where that is 0. */
-int64_t iq_int8_linear_workspace(int64_t tokens, int64_t depth);
+ * and scales between the two, iq_int8_linear_workspace(tokens, channels, depth)
+ * bytes, 16-byte aligned; it may be NULL where that is 0. */
+int64_t iq_int8_linear_workspace(int64_t tokens, int64_t channels, int64_t depth);
 iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const int8_t* w,
                            int64_t ldw, const float* w_scale, int64_t tokens, int64_t channels,
                            int64_t depth, void* y, int64_t ldy, void* workspace,

@@ -79,12 +79,14 @@ def test_int8_matmul_refusals(lib):
 
 
 def test_int8_linear_refusals(lib):
-    need = lib.iq_int8_linear_workspace(40, 70)
+    need = lib.iq_int8_linear_workspace(40, 8, 70)
     assert need == 40 * 80 + 160
-    assert lib.iq_int8_linear_workspace(4, 70) == 0                      # a few tokens: none
-    assert lib.iq_int8_linear_workspace(0, 70) == 0
-    assert lib.iq_int8_linear_workspace(4, 0) == 0
-    assert lib.iq_int8_linear_workspace(4, 131072) == 0
+    assert lib.iq_int8_linear_workspace(4, 8, 70) == 0                   # a few tokens: none
+    assert lib.iq_int8_linear_workspace(4, 8 << 20, 70) == 4 * 80 + 16   # on a wide weight
+    assert lib.iq_int8_linear_workspace(0, 8, 70) == 0
+    assert lib.iq_int8_linear_workspace(4, 0, 70) == 0
+    assert lib.iq_int8_linear_workspace(4, 8, 0) == 0
+    assert lib.iq_int8_linear_workspace(4, 8, 131072) == 0
 
     def f(dt=1, x=FAKE, ldx=70, w=FAKE, ldw=70, ws=FAKE, t=40, n=8, k=70, y=FAKE, ldy=8, wk=FAKE,
           wb=need, st=FAKE):
