@@ -340,7 +340,15 @@ __global__ __launch_bounds__(kWT* kWC* kWK* kWave, kWT* kWC* kWK / 4) void int8_
     };
 
     if constexpr (kDirect) {
+        // Where a weight is read once, each channel tile begins at a step of its
+        // own and ends with those before it: rows that are a power of two apart
+        // share HBM channels, and tiles that go through the depth together meet
+        // there (16 tokens, 2 of 8 experts of 2048 x 4096: 20 us, so 16).  Large
+        // tiles share the tokens' L2 lines by going together (58 us so, 55).
+        const int shift = (kExperts ? kRows <= 128 : p.rows <= kRows) && steps
+                              ? t.channel_tile * 7 % steps : 0;
         auto fetch = [&](int b, int step) {
+            step += step + shift < steps ? shift : shift - steps;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 copy_to_lds(from[i] + (int64_t)step * kDepth,
@@ -551,21 +559,16 @@ int64_t workgroups(const Int8Product& p, int rows, int channel_tiles)
 }
 
 template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int kStages,
-          bool kPingPong, bool kDirect>
+          bool kPingPong, bool kDirect, bool kExperts>
 hipError_t launch_tiles(const Int8Product& p, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
     const int64_t wgs = workgroups(p, kRows, channel_tiles);
     if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)wgs), threads(kWT * kWC * kWK * kWave);
-    if (p.experts)
-        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
-                                             kPingPong, kDirect, true>),
-                           grid, threads, 0, stream, p, channel_tiles);
-    else
-        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
-                                             kPingPong, kDirect, false>),
-                           grid, threads, 0, stream, p, channel_tiles);
+    hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
+                                         kPingPong, kDirect, kExperts>),
+                       dim3((unsigned)wgs), dim3(kWT * kWC * kWK * kWave), 0, stream, p,
+                       channel_tiles);
     return hipGetLastError();
 }
 
@@ -612,21 +615,21 @@ constexpr TileTime kDense[] = {
     {128, 256, 2.79, 3.13, 5.56, 4.49, 1.71},
     {192, 192, 3.49, 4.42, 5.03, 3.57, 2.50},
     {256, 256, 3.42, 8.79, 5.83, 4.41, 5.17}};
-// Likewise for products by expert, 1 to 4096 tokens of 2 and 8 choices, 8, 16
-// and 64 experts, chosen evenly and not: 3 % longer than the fastest.  Tiles take
-// longer than in a dense product, their weight coming from HBM.
+// Likewise for 540 products by expert, 1 to 4096 tokens of 1, 2 and 8 choices, 8 to
+// 128 experts, chosen evenly and not, weights out of HBM: 4 % longer than the
+// fastest of fifteen sizes on average, 55 % at worst, where a distribution needs
+// just over a round of tiles.  Tiles take longer than in a dense product.
 constexpr TileTime kByExpert[] = {
-    {16, 16, 4.26, 0.0, 0.46, 0.61, 0.0},
-    {32, 32, 4.14, 0.0, 0.78, 1.35, 0.20},
-    {64, 64, 2.89, 1.81, 1.41, 2.73, 0.75},
-    {64, 128, 4.44, 0.0, 2.25, 5.29, 0.75},
-    {64, 192, 5.12, 0.05, 3.24, 6.65, 0.53},
-    {128, 128, 4.98, 0.0, 2.79, 6.54, 1.07},
-    {128, 192, 3.11, 3.45, 4.33, 5.62, 0.97},
-    {192, 128, 3.33, 2.96, 3.62, 4.81, 1.62},
-    {128, 256, 5.08, 0.65, 5.31, 7.97, 2.93},
-    {192, 192, 1.43, 6.58, 4.15, 3.36, 3.72},
-    {256, 256, 8.13, 3.32, 5.92, 6.39, 5.38}};
+    {16, 16, 4.28, 0.0, 0.58, 0.55, 0.0},
+    {32, 64, 4.91, 0.0, 1.62, 1.24, 0.41},
+    {32, 128, 7.13, 0.0, 1.85, 1.17, 1.47},
+    {64, 64, 5.04, 0.0, 1.98, 1.78, 0.32},
+    {64, 128, 4.59, 0.0, 2.82, 4.69, 1.23},
+    {64, 192, 5.45, 0.0, 3.83, 5.50, 1.58},
+    {128, 128, 4.74, 0.0, 3.06, 6.10, 2.20},
+    {128, 192, 3.32, 3.04, 4.62, 5.46, 2.22},
+    {192, 192, 1.31, 6.45, 4.83, 3.57, 4.39},
+    {256, 256, 6.35, 6.70, 5.26, 3.39, 8.68}};
 // And where rows do not start on 16 bytes: 2 % longer than the fastest.
 constexpr TileTime kUnaligned[] = {
     {16, 16, 7.38, 0.34, 0.84, 0.46, 0.0},
@@ -651,6 +654,33 @@ int choose_tile(const Int8Product& p, int cus, const TileTime (&tiles)[kN])
     return tiles[best].rows * 1000 + tiles[best].channels;
 }
 
+template <bool kExperts>
+hipError_t launch_unaligned(const Int8Product& p, int cus, hipStream_t stream)
+{
+    switch (choose_tile(p, cus, kUnaligned)) {
+    case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 2, false, false, kExperts>(p, stream);
+    case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 2, false, false, kExperts>(p, stream);
+    case 64064: return launch_tiles<64, 64, 4, 2, 1, 128, 2, false, false, kExperts>(p, stream);
+    case 128128: return launch_tiles<128, 128, 4, 4, 1, 128, 2, false, false, kExperts>(p, stream);
+    default: return launch_tiles<128, 256, 2, 4, 1, 64, 2, false, false, kExperts>(p, stream);
+    }
+}
+
+// The tiles that both kinds of product take; `tile` as choose_tile gives it.
+template <bool kExperts>
+hipError_t launch_direct(int tile, const Int8Product& p, hipStream_t stream)
+{
+    switch (tile) {
+    case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 4, false, true, kExperts>(p, stream);
+    case 64128: return launch_tiles<64, 128, 2, 4, 1, 128, 4, true, true, kExperts>(p, stream);
+    case 64192: return launch_tiles<64, 192, 4, 2, 1, 128, 4, true, true, kExperts>(p, stream);
+    case 128128: return launch_tiles<128, 128, 4, 2, 1, 128, 4, true, true, kExperts>(p, stream);
+    case 128192: return launch_tiles<128, 192, 4, 2, 1, 128, 3, true, true, kExperts>(p, stream);
+    case 192192: return launch_tiles<192, 192, 4, 2, 1, 64, 4, true, true, kExperts>(p, stream);
+    default: return launch_tiles<256, 256, 4, 2, 1, 64, 4, true, true, kExperts>(p, stream);
+    }
+}
+
 }  // namespace
 
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream)
@@ -660,27 +690,25 @@ hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream
                         (p.experts <= 1 || p.w_stride % 16 == 0) &&
                         reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
-    if (!direct) {
-        switch (choose_tile(p, cus, kUnaligned)) {
-        case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 2, false, false>(p, stream);
-        case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 2, false, false>(p, stream);
-        case 64064: return launch_tiles<64, 64, 4, 2, 1, 128, 2, false, false>(p, stream);
-        case 128128: return launch_tiles<128, 128, 4, 4, 1, 128, 2, false, false>(p, stream);
-        default: return launch_tiles<128, 256, 2, 4, 1, 64, 2, false, false>(p, stream);
+    if (!direct)
+        return p.experts ? launch_unaligned<true>(p, cus, stream)
+                         : launch_unaligned<false>(p, cus, stream);
+    if (p.experts) {
+        // Tiles of few rows, several workgroups to a compute unit: it is the
+        // number of loads under way that counts on weights out of HBM.
+        switch (const int tile = choose_tile(p, cus, kByExpert)) {
+        case 32064: return launch_tiles<32, 64, 1, 4, 1, 128, 4, false, true, true>(p, stream);
+        case 32128: return launch_tiles<32, 128, 1, 4, 1, 128, 3, false, true, true>(p, stream);
+        case 64064: return launch_tiles<64, 64, 2, 2, 1, 128, 4, false, true, true>(p, stream);
+        default: return launch_direct<true>(tile, p, stream);
         }
     }
-    switch (p.experts ? choose_tile(p, cus, kByExpert) : choose_tile(p, cus, kDense)) {
-    case 16016: return launch_tiles<16, 16, 1, 1, 4, 256, 4, false, true>(p, stream);
-    case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 4, false, true>(p, stream);
-    case 64064: return launch_tiles<64, 64, 4, 2, 1, 256, 4, true, true>(p, stream);
-    case 64128: return launch_tiles<64, 128, 2, 4, 1, 128, 4, true, true>(p, stream);
-    case 64192: return launch_tiles<64, 192, 4, 2, 1, 128, 4, true, true>(p, stream);
-    case 128128: return launch_tiles<128, 128, 4, 2, 1, 128, 4, true, true>(p, stream);
-    case 128192: return launch_tiles<128, 192, 4, 2, 1, 128, 3, true, true>(p, stream);
-    case 192128: return launch_tiles<192, 128, 4, 2, 1, 128, 3, true, true>(p, stream);
-    case 192192: return launch_tiles<192, 192, 4, 2, 1, 64, 4, true, true>(p, stream);
-    case 128256: return launch_tiles<128, 256, 2, 4, 1, 64, 4, true, true>(p, stream);
-    default: return launch_tiles<256, 256, 4, 2, 1, 64, 4, true, true>(p, stream);
+    switch (const int tile = choose_tile(p, cus, kDense)) {
+    case 32032: return launch_tiles<32, 32, 2, 2, 2, 256, 4, false, true, false>(p, stream);
+    case 64064: return launch_tiles<64, 64, 4, 2, 1, 256, 4, true, true, false>(p, stream);
+    case 192128: return launch_tiles<192, 128, 4, 2, 1, 128, 3, true, true, false>(p, stream);
+    case 128256: return launch_tiles<128, 256, 2, 4, 1, 64, 4, true, true, false>(p, stream);
+    default: return launch_direct<false>(tile, p, stream);
     }
 }
 

@@ -175,7 +175,8 @@ LARGE = [(33, 300, 528), (700, 515, 1000), (500, 2049, 528), (700, 2049, 1000), 
          (1000, 2049, 1000), (2100, 2049, 528), (1300, 4100, 1000), (2600, 2049, 1000), (4100, 2049, 528),
          (4100, 2600, 2050), (190, 4100, 528), (3300, 515, 136), (130, 1540, 1000), (45, 515, 776),
          (70, 1030, 264), (100, 2049, 264), (4265, 403, 144), (978, 5530, 144), (1052, 5530, 144),
-         (2366, 5197, 144), (90, 5530, 144), (164, 5530, 528), (127, 4531, 144)]
+         (2366, 5197, 144), (90, 5530, 144), (164, 5530, 528), (127, 4531, 144),
+         (9, 10990, 152), (203, 253, 152), (101, 5932, 528)]
 
 
 def exact_product(x, xs, w, ws):
