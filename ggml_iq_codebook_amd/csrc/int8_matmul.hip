@@ -255,8 +255,11 @@ __device__ __forceinline__ void wait_and_meet()
 // reach 3250 TOP/s (4480 on zeros), and this kernel takes 51 us for 4096^3 zeros.
 // Ping-pong against waves that all wait, read and multiply together: 62 us
 // against 74; v_mfma_i32_32x32x32_i8 in its place: 71.
-// Small tiles are bound by the latency of their first loads, products by expert
-// of few rows by HBM (16 tokens, 2 of 16 experts of 1536 x 4096: 18 us, 5.5 TB/s).
+// Small tiles are bound by the latency of their first loads and by what a compute
+// unit loads from the L2 (about 38 bytes a clock), so small products take many
+// small tiles: 24 x 1536 x 4096 in a graph 4.3 us with 16 x 16 tiles, 6.1 with
+// 32 x 32.  Products by expert of few rows are bound by HBM (16 tokens, 2 of 16
+// experts of 1536 x 4096: 16 us, 6.2 TB/s).
 template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int kStages,
           bool kPingPong, bool kDirect, bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWK* kWave, kWT* kWC* kWK / 4) void int8_tile_kernel(
