@@ -10,7 +10,7 @@
 // of 64 bytes a row under way at once.  The 8 partial sums are integers, so
 // adding them in LDS is exact.
 //
-// One token through 4096 x 4096: 7.6 us in a graph with its weight in HBM, as two
+// One token through 4096 x 4096: 7.8 us in a graph with its weight in HBM, as two
 // launches 10.0; called back to back on a weight that stays in the caches 6.2 us
 // (16.8 MB at the rate of a large copy: 3.3 us).  32 or 64 channels to a
 // workgroup, which halve the rounding of wide weights, took 9.4 and 14.0 us here
@@ -31,23 +31,33 @@ constexpr int kTokens = 16;           // columns of the matrix instruction
 constexpr int kChannels = kDecodeChannels;   // and its rows
 constexpr int kFlight = 8;            // pieces of the weight under way
 constexpr int kPart = kWave * kChunk; // values a wave rounds at once
-constexpr int kKeep = kDecodeParts / kWaves;
 
-// 16 bytes of a row from depth `at`, zeros beyond its end, at any alignment.
+// 16 bytes of a row from depth `at`.  Beyond its end there are zeros, or, where
+// the depth is a multiple of 16 (kWhole), the row's last values: the tokens'
+// codes are zeros there.
+template <bool kWhole>
 __device__ __forceinline__ v4i load_codes(const int8_t* row, int at, int depth)
 {
     v4i v = {0, 0, 0, 0};
-    if (at + 16 <= depth) {
-        __builtin_memcpy(&v, row + at, 16);
+    if (kWhole || at + 16 <= depth) {
+        __builtin_memcpy(&v, row + (kWhole ? min(at, depth - 16) : at), 16);
     } else if (at < depth) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (at + i < depth) v[i / 4] |= (int)((uint32_t)(uint8_t)row[at + i] << (8 * (i % 4)));
+        uint64_t u[2] = {0u, 0u};
+#pragma unroll 1
+        for (int i = 0; i < depth - at; ++i) {
+            const uint64_t byte = (uint64_t)(uint8_t)row[at + i] << (8 * (i % 8));
+            u[0] |= i < 8 ? byte : 0u;
+            u[1] |= i < 8 ? 0u : byte;
+        }
+        v = {(int)u[0], (int)(u[0] >> 32), (int)u[1], (int)(u[1] >> 32)};
     }
     return v;
 }
 
-template <int kDT, bool kWhole>
+// kKeep: how many parts a wave rounds at most.  Its code is read once by every
+// compute unit, so that its size shows: one token through 8192 x 512 takes 4.3 us
+// with 4 KB of it; with 22 KB, for four parts and any depth, it took 5.6.
+template <int kDT, bool kWhole, int kKeep>
 __global__ __launch_bounds__(kThreads) void int8_decode_kernel(Int8Product p, const void* x,
                                                                int64_t ldx, int32_t* status)
 {
@@ -67,10 +77,11 @@ __global__ __launch_bounds__(kThreads) void int8_decode_kernel(Int8Product p, co
     const int channel = blockIdx.x * kChannels + lane % 16;
     const int quarter = lane / 16;
     const int8_t* w = p.w + (int64_t)min(channel, p.channels - 1) * p.ldw;
-    v4i a[kFlight];
+    v4i a[kFlight] = {};
 #pragma unroll
     for (int i = 0; i < kFlight; ++i)
-        a[i] = load_codes(w, first + i < last ? (first + i) * 64 + quarter * 16 : p.depth, p.depth);
+        if (first + i < last)
+            a[i] = load_codes<kWhole>(w, (first + i) * 64 + quarter * 16, p.depth);
 
     // The tokens, in parts of kPart values dealt out to the waves.
     const int parts = (p.depth + kPart - 1) / kPart;
@@ -124,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void int8_decode_kernel(Int8Product p, co
                 acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b, acc, 0, 0, 0);
             }
             const int next = at + i + kFlight;
-            if (next < last) a[i] = load_codes(w, next * 64 + quarter * 16, p.depth);
+            if (next < last) a[i] = load_codes<kWhole>(w, next * 64 + quarter * 16, p.depth);
         }
     }
     *reinterpret_cast<v4i*>(&sums[wave][lane % 16][4 * quarter]) = acc;
@@ -140,23 +151,33 @@ __global__ __launch_bounds__(kThreads) void int8_decode_kernel(Int8Product p, co
     }
 }
 
-}  // namespace
-
-hipError_t launch_int8_decode(const Int8Product& p, int dtype, const void* x, int64_t ldx,
-                              int32_t* status, hipStream_t stream)
+template <int kKeep>
+hipError_t launch_keeping(const Int8Product& p, int dtype, const void* x, int64_t ldx,
+                          int32_t* status, hipStream_t stream)
 {
     const unsigned wgs = (unsigned)((p.channels + kChannels - 1) / kChannels);
     const size_t lds = (size_t)p.tokens * decode_stride(p.depth);
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
-        if (p.depth % kChunk == 0)
-            hipLaunchKernelGGL((int8_decode_kernel<kDT, true>), dim3(wgs), dim3(kThreads), lds,
-                               stream, p, x, ldx, status);
+        if (p.depth % 16 == 0)
+            hipLaunchKernelGGL((int8_decode_kernel<kDT, true, kKeep>), dim3(wgs), dim3(kThreads),
+                               lds, stream, p, x, ldx, status);
         else
-            hipLaunchKernelGGL((int8_decode_kernel<kDT, false>), dim3(wgs), dim3(kThreads), lds,
-                               stream, p, x, ldx, status);
+            hipLaunchKernelGGL((int8_decode_kernel<kDT, false, kKeep>), dim3(wgs), dim3(kThreads),
+                               lds, stream, p, x, ldx, status);
         return hipGetLastError();
     });
+}
+
+}  // namespace
+
+hipError_t launch_int8_decode(const Int8Product& p, int dtype, const void* x, int64_t ldx,
+                              int32_t* status, hipStream_t stream)
+{
+    const int64_t parts = p.tokens * ((p.depth + kPart - 1) / kPart);
+    if (parts <= kWaves) return launch_keeping<1>(p, dtype, x, ldx, status, stream);
+    if (parts <= 2 * kWaves) return launch_keeping<2>(p, dtype, x, ldx, status, stream);
+    return launch_keeping<kDecodeParts / kWaves>(p, dtype, x, ldx, status, stream);
 }
 
 }  // namespace iqk

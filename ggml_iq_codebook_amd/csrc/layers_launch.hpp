@@ -52,11 +52,11 @@ __host__ __device__ constexpr int decode_stride(int depth)
 // units.  GPU time, one launch against two, us (as calls of their own the second
 // launch adds 3 more):
 //   channels x depth, tokens   1            2            4            8
-//   1024 x 1024                4.3 / 6.0    4.6 / 6.2    4.8 / 6.2    5.9 / 6.4
-//   4096 x 4096                7.6 / 10.0   8.5 / 9.8   10.5 / 9.9
-//   5632 x 2048                7.2 / 7.8    7.8 / 7.9    9.3 / 8.0
+//   1024 x 1024                3.6 / 6.0                              5.0 / 6.4
+//   4096 x 4096                7.8 / 10.0   8.8 / 9.8   10.5 / 9.9
+//   5632 x 2048                6.3 / 7.8    6.6 / 7.9    9.3 / 8.0
 //   4096 x 16384              19.2 / 25.5
-//   16384 x 4096              17.7 / 19.7  19.0 / 18.9  21.5 / 19.2
+//   16384 x 4096              17.4 / 19.7  19.0 / 18.9  21.5 / 19.2
 //   32768 x 2048              21.3 / 18.7
 inline bool int8_decode_takes(int64_t tokens, int64_t channels, int64_t depth)
 {

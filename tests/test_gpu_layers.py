@@ -268,7 +268,8 @@ def test_product_of_no_tokens():
                                                    (200, 515, 1001), (16, 75, 1024), (16, 75, 1025),
                                                    (4, 64, 4096), (3, 40, 7), (1, 20, 16384),
                                                    (1, 20, 16385), (11, 1, 513), (2, 4097, 8), (8, 50, 1024),
-                                                   (2, 40, 4096), (3, 16384, 100), (3, 16385, 100)])
+                                                   (2, 40, 4096), (3, 16384, 100), (3, 16385, 100),
+                                                   (1, 20, 12345), (8, 50, 1000)])
 def test_linear(dtype, tokens, channels, depth):
     x = normal((tokens, depth), tokens + depth, dtype)
     w, ws = iq.quantize_rows(normal((channels, depth), channels))
