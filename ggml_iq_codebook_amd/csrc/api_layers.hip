@@ -30,7 +30,7 @@ bool bad_rows(int64_t rows, int64_t cols, int64_t ld, bool output)
     return cols > most || (ld > 0 && rows > most / ld);
 }
 
-// Launches have at most 2^31 - 1 workgroups, and places are 32-bit.
+// Places are 32-bit.
 bool bad_choices(int64_t tokens, int32_t top_k)
 {
     return tokens < 0 || top_k < 1 || tokens > INT32_MAX / top_k;
@@ -52,7 +52,7 @@ int64_t code_stride(int64_t depth) { return round_up(depth, 16); }
 iqk::Route route(iq_dtype_t dtype, int64_t tokens, int64_t width, const int32_t* position,
                  int32_t top_k, const int32_t* offsets, int32_t experts)
 {
-    return {tokens, width, position, top_k, offsets + experts,
+    return {tokens, tokens * top_k, width, position, top_k, offsets + experts,
             iqk::streams(tokens * top_k, width, value_bytes(dtype))};
 }
 

@@ -233,7 +233,7 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ int64_t place_of(const Route& r, int64_t token, int j)
 {
     const int32_t p = r.position[token * r.top_k + j];
-    return p >= 0 && p < r.tokens * r.top_k ? p : -1;
+    return p >= 0 && p < r.rows ? p : -1;
 }
 
 // This thread's token.  Where a row is shared by whole waves the token is the
@@ -296,10 +296,9 @@ struct Choices {
             p[g] = r.position[c];
             weight[g] = weights ? weights[c] : 1.0f;
         }
-        const int64_t rows = r.tokens * r.top_k;
 #pragma unroll
         for (int g = 0; g < kGroup; ++g) {
-            const bool there = (j0 + g < r.top_k) & (p[g] >= 0) & (p[g] < rows);
+            const bool there = (j0 + g < r.top_k) & (p[g] >= 0) & (p[g] < r.rows);
             place[g] = there ? p[g] : -1;
             live[g] = there & (p[g] < kept);
             row[g] = live[g] ? p[g] : 0;
@@ -451,6 +450,22 @@ int lanes_for(int64_t width, int values)
     return lanes;
 }
 
+// launch(the tokens from `token` on, token, workgroups) for each part of a launch
+// that gives a token to `lanes` threads.
+template <class Launch>
+hipError_t by_tokens(const Route& r, int lanes, Launch&& launch)
+{
+    const int each = kThreads / lanes;
+    return in_parts((r.tokens + each - 1) / each, kThreads, [&](int64_t first, dim3 wgs) {
+        const int64_t token = first * each;
+        Route part = r;
+        part.tokens -= token;
+        part.position += token * r.top_k;
+        launch(part, token, wgs);
+        return hipGetLastError();
+    });
+}
+
 }  // namespace
 
 // One workgroup while a wave's part fits its registers; beyond, a workgroup per
@@ -516,13 +531,15 @@ hipError_t launch_expert_dispatch(int dtype, const Route& r, const void* x, int6
     return with_dtype(dtype, [&](auto dt) {
         constexpr int kDT = decltype(dt)::value;
         const int lanes = lanes_for(r.width, Row<kDT>::kN);
-        const dim3 wgs((unsigned)((r.tokens + kThreads / lanes - 1) / (kThreads / lanes)));
         const auto kernel = lanes < kWave ? (r.streaming ? expert_dispatch_kernel<kDT, false, true>
                                                          : expert_dispatch_kernel<kDT, false, false>)
                                           : (r.streaming ? expert_dispatch_kernel<kDT, true, true>
                                                          : expert_dispatch_kernel<kDT, true, false>);
-        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, r, x, ldx, sorted, lds, lanes);
-        return hipGetLastError();
+        return by_tokens(r, lanes, [&](const Route& part, int64_t token, dim3 wgs) {
+            hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, part,
+                               static_cast<const typename Value<kDT>::raw*>(x) + token * ldx, ldx,
+                               sorted, lds, lanes);
+        });
     });
 }
 
@@ -530,10 +547,12 @@ template <int kDT, bool kWeighted, int kGroup, bool kWaves>
 static hipError_t combine_as(const Route& r, const void* y, int64_t ldy, const float* weights,
                              void* out, int64_t ldo, int lanes, hipStream_t stream)
 {
-    const dim3 wgs((unsigned)((r.tokens + kThreads / lanes - 1) / (kThreads / lanes)));
-    hipLaunchKernelGGL((expert_combine_kernel<kDT, kWeighted, kGroup, kWaves>), wgs,
-                       dim3(kThreads), 0, stream, r, y, ldy, weights, out, ldo, lanes);
-    return hipGetLastError();
+    return by_tokens(r, lanes, [&](const Route& part, int64_t token, dim3 wgs) {
+        hipLaunchKernelGGL((expert_combine_kernel<kDT, kWeighted, kGroup, kWaves>), wgs,
+                           dim3(kThreads), 0, stream, part, y, ldy,
+                           kWeighted ? weights + token * r.top_k : nullptr,
+                           static_cast<typename Value<kDT>::raw*>(out) + token * ldo, ldo, lanes);
+    });
 }
 
 // As many rows at once as there are choices, 2, 4 or 8; 4 where lanes of a wave
@@ -571,16 +590,18 @@ hipError_t launch_expert_combine_backward(int dtype, const Route& r, const void*
         constexpr int kDT = decltype(dt)::value;
         // Two vectors a lane of a wave at most, else the workgroup.
         const bool by_wave = r.width <= 2 * kWave * Row<kDT>::kN;
-        constexpr int kTokens = kThreads / kWave;
-        const dim3 wgs((unsigned)(by_wave ? (r.tokens + kTokens - 1) / kTokens : r.tokens));
         const auto kernel =
             by_wave ? (r.streaming ? expert_combine_backward_kernel<kDT, kWave, true>
                                    : expert_combine_backward_kernel<kDT, kWave, false>)
                     : (r.streaming ? expert_combine_backward_kernel<kDT, kThreads, true>
                                    : expert_combine_backward_kernel<kDT, kThreads, false>);
-        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, r, out_grad, ldo, y, ldy,
-                           weights, y_grad, ldg, weights_grad);
-        return hipGetLastError();
+        return by_tokens(r, by_wave ? kWave : kThreads,
+                         [&](const Route& part, int64_t token, dim3 wgs) {
+            hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, part,
+                               static_cast<const typename Value<kDT>::raw*>(out_grad) + token * ldo,
+                               ldo, y, ldy, weights + token * r.top_k, y_grad, ldg,
+                               weights_grad + token * r.top_k);
+        });
     });
 }
 

@@ -60,7 +60,7 @@ __device__ __forceinline__ Tile dense_tile(const Int8Product& p, int channel_til
     // Bands of kBand row tiles, channel tile by channel tile.
     constexpr int kBand = 8;
     const int64_t row_tiles = (p.rows + kRows - 1) / kRows;
-    const int64_t id = by_xcd(blockIdx.x, row_tiles * channel_tiles);
+    const int64_t id = by_xcd(p.first_tile + blockIdx.x, row_tiles * channel_tiles);
     const int64_t band = id / (kBand * (int64_t)channel_tiles);
     const int64_t in_band = id - band * kBand * channel_tiles;
     const int64_t height = min((int64_t)kBand, row_tiles - band * kBand);
@@ -102,8 +102,8 @@ __device__ __forceinline__ Tile expert_tile(const Int8Product& p, int channel_ti
     }
     Tile t = {0, 0, 0, -2};
     const int64_t tiles = (int64_t)total * channel_tiles;
-    if ((int64_t)blockIdx.x >= tiles) return t;
-    const int64_t id = by_xcd(blockIdx.x, tiles);
+    if (p.first_tile + blockIdx.x >= tiles) return t;
+    const int64_t id = by_xcd(p.first_tile + blockIdx.x, tiles);
     const int row_tile = (int)(id / channel_tiles);
     t.channel_tile = (int)(id - (int64_t)row_tile * channel_tiles);
     int before = 0;
@@ -566,13 +566,15 @@ template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int k
 hipError_t launch_tiles(const Int8Product& p, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
-    const int64_t wgs = workgroups(p, kRows, channel_tiles);
-    if (wgs > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
-                                         kPingPong, kDirect, kExperts>),
-                       dim3((unsigned)wgs), dim3(kWT * kWC * kWK * kWave), 0, stream, p,
-                       channel_tiles);
-    return hipGetLastError();
+    constexpr int kThreads = kWT * kWC * kWK * kWave;
+    Int8Product part = p;
+    return in_parts(workgroups(p, kRows, channel_tiles), kThreads, [&](int64_t first, dim3 wgs) {
+        part.first_tile = first;
+        hipLaunchKernelGGL((int8_tile_kernel<kRows, kChannels, kWT, kWC, kWK, kDepth, kStages,
+                                             kPingPong, kDirect, kExperts>),
+                           wgs, dim3(kThreads), 0, stream, part, channel_tiles);
+        return hipGetLastError();
+    });
 }
 
 // The expected time of a tile size in microseconds: `once` for the product, and

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch_parts.hpp"
+
 namespace iqk {
 
 hipError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols,
@@ -33,6 +35,7 @@ struct Int8Product {
     const int32_t* offsets;
     int experts;
     int top_k;
+    int64_t first_tile = 0;   // of the launch's part of the tiles
 };
 
 hipError_t launch_int8_product(const Int8Product& p, int cus, hipStream_t stream);
@@ -80,6 +83,7 @@ hipError_t launch_expert_sort(const void* choice, int choice_bytes, int64_t n, i
 
 struct Route {
     int64_t tokens;
+    int64_t rows;             // of a sorted tensor
     int64_t width;
     const int32_t* position;
     int top_k;

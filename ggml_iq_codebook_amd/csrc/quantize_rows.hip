@@ -96,14 +96,16 @@ template <int kDT, int kLanes, int kKeep>
 hipError_t launch(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* q, int64_t ldq,
                   float* scale, int32_t* status, hipStream_t stream)
 {
-    const int64_t wgs = (rows + kThreads / kLanes - 1) / (kThreads / kLanes);
-    if (cols % kChunk == 0)
-        hipLaunchKernelGGL((quantize_rows_kernel<kDT, kLanes, kKeep, true>), dim3((unsigned)wgs),
-                           dim3(kThreads), 0, stream, x, ldx, rows, cols, q, ldq, scale, status);
-    else
-        hipLaunchKernelGGL((quantize_rows_kernel<kDT, kLanes, kKeep, false>), dim3((unsigned)wgs),
-                           dim3(kThreads), 0, stream, x, ldx, rows, cols, q, ldq, scale, status);
-    return hipGetLastError();
+    constexpr int kRows = kThreads / kLanes;
+    const auto kernel = cols % kChunk == 0 ? quantize_rows_kernel<kDT, kLanes, kKeep, true>
+                                           : quantize_rows_kernel<kDT, kLanes, kKeep, false>;
+    return in_parts((rows + kRows - 1) / kRows, kThreads, [&](int64_t first, dim3 wgs) {
+        const int64_t row = first * kRows;
+        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream,
+                           static_cast<const typename Value<kDT>::raw*>(x) + row * ldx, ldx,
+                           rows - row, cols, q + row * ldq, ldq, scale + row, status);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
