@@ -17,6 +17,7 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "launch_parts.hpp"
 
 namespace iqk {
 namespace {
@@ -136,18 +137,16 @@ __global__ __launch_bounds__(kThreads) void dequant_iq1m_kernel(const uint8_t* _
 hipError_t launch_dequant(int fmt, const uint8_t* packed, const float* grid, int grid_size,
                           float* out, int32_t* status, const BlockGeom& g, hipStream_t stream)
 {
-    const int64_t nquads = g.nblocks * 64;
-    const int64_t wgs = (nquads + kThreads - 1) / kThreads;
-    if (fmt == IQ_FMT_IQ1_S)
-        hipLaunchKernelGGL(dequant_iq1s_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream,
-                           packed, grid, grid_size, out, status, nquads);
-    else if (fmt == IQ_FMT_IQ1_M)
-        hipLaunchKernelGGL(dequant_iq1m_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream,
-                           packed, grid, grid_size, out, status, nquads);
-    else
-        hipLaunchKernelGGL(dequant_iq2xs_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, stream,
-                           packed, grid, grid_size, out, status, nquads);
-    return hipGetLastError();
+    const auto kernel = fmt == IQ_FMT_IQ1_S ? dequant_iq1s_kernel
+                        : fmt == IQ_FMT_IQ1_M ? dequant_iq1m_kernel : dequant_iq2xs_kernel;
+    const int block_bytes = fmt == IQ_FMT_IQ1_S ? 50 : fmt == IQ_FMT_IQ1_M ? 56 : 74;
+    constexpr int kBlocks = kThreads / 64;        // of a workgroup
+    return in_parts((g.nblocks + kBlocks - 1) / kBlocks, kThreads, [&](int64_t first, dim3 wgs) {
+        const int64_t block = first * kBlocks;
+        hipLaunchKernelGGL(kernel, wgs, dim3(kThreads), 0, stream, packed + block * block_bytes,
+                           grid, grid_size, out + block * 256, status, (g.nblocks - block) * 64);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace iqk
