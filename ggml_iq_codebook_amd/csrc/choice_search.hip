@@ -37,6 +37,7 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "launch_parts.hpp"
 
 namespace iqk {
 namespace {
@@ -54,7 +55,8 @@ struct SearchArgs {
     const float* cand;       // [rows][nblk][G][C][L]
     int32_t* picks;          // [rows][nblk][G]
     int32_t* trace;          // NULL or [sweeps+1][rows][nblk][G]
-    int64_t rows;
+    int64_t rows;            // of this launch
+    int64_t slot_rows;       // of the whole call: of one slot of the trace
     int64_t nblk;
     int C, sweeps;
 };
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void choice_search_kernel(SearchArgs a)
     const int64_t cstride = a.nblk * G * C * L;   // floats per row of cand
     const float* __restrict__ cb = a.cand + blk * (int64_t)G * C * L;
     auto out_index = [&](int64_t slot, int64_t row, int g) -> int64_t {
-        return ((slot * a.rows + row) * a.nblk + blk) * G + g;
+        return ((slot * a.slot_rows + row) * a.nblk + blk) * G + g;
     };
     auto cand_ptr = [&](int rr, int g, int c) -> const float* {
         return cb + (row0 + rr) * cstride + ((int64_t)g * C + c) * L;
@@ -516,13 +518,15 @@ hipError_t launch_choice_search(const float* H, const float* cand, int64_t rows,
                                 int G, int C, int sweeps, int32_t* picks, int32_t* trace,
                                 hipStream_t stream)
 {
-    SearchArgs a{H, cand, picks, trace, rows, nblk, C, sweeps};
-    const dim3 grid((unsigned)((rows + kRows - 1) / kRows), (unsigned)nblk);
-    if (G == 16)
-        hipLaunchKernelGGL(choice_search_kernel<16>, grid, dim3(kThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL(choice_search_kernel<32>, grid, dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+    const auto kernel = G == 16 ? choice_search_kernel<16> : choice_search_kernel<32>;
+    return in_parts((rows + kRows - 1) / kRows, kThreads, [&](int64_t first, dim3 wgs) {
+        const int64_t row = first * kRows;
+        const SearchArgs a{H, cand + row * nblk * C * 256, picks + row * nblk * G,
+                           trace ? trace + row * nblk * G : nullptr, rows - row, rows, nblk, C,
+                           sweeps};
+        hipLaunchKernelGGL(kernel, dim3(wgs.x, (unsigned)nblk), dim3(kThreads), 0, stream, a);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace iqk

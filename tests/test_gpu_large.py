@@ -45,3 +45,20 @@ def test_decode(fmt):
     out = out.view(times, *want.shape)
     for first in range(0, times, 1024):
         assert bool((out[first:first + 1024] == want).all()), first
+
+
+def test_choice_search():
+    """2^27 + 40 rows, 32 threads each, of one candidate of zeros: every pick is that one,
+    and so is every entry of the trace."""
+    needs(160)
+    rows, groups, sweeps = 2 ** 27 + 40, 8, 1
+    H = torch.eye(256, device=DEV)
+    cand = torch.zeros((rows, 256), device=DEV)
+    picks = torch.full((rows, groups), 7, dtype=torch.int32, device=DEV)
+    trace = torch.full((sweeps + 1, rows, groups), 7, dtype=torch.int32, device=DEV)
+    P = ctypes.c_void_p
+    code = iq.load().iq_choice_search(P(H.data_ptr()), P(cand.data_ptr()), rows, groups, 1, sweeps,
+                                      P(picks.data_ptr()), P(trace.data_ptr()),
+                                      P(torch.cuda.current_stream().cuda_stream))
+    assert code == 0
+    assert not picks.any() and not trace.any()
