@@ -7,10 +7,14 @@
 #include "api_common.hpp"
 #include "iq_layers.h"
 #include "layers_launch.hpp"
+#include "overlap.hpp"
 
 using iqk::aligned;
+using iqk::array;
 using iqk::check_device;
 using iqk::from_hip;
+using iqk::overlaps;
+using iqk::region;
 using iqk::run_with_status;
 
 namespace {
@@ -57,7 +61,7 @@ iqk::Route route(iq_dtype_t dtype, int64_t tokens, int64_t width, const int32_t*
 }
 
 // One tensor of a routing call: [tokens][width], or [tokens * top_k][width]
-// where it is sorted.
+// where it is sorted.  The output comes last.
 struct Rows {
     const void* p;
     int64_t ld;
@@ -87,6 +91,27 @@ iq_status_t route_args(iq_dtype_t dtype, int64_t tokens, int64_t width, int32_t 
     return IQ_OK;
 }
 
+// Whether the last of the tensors, the output, or the weights' gradient overlaps
+// something else of the call.
+template <int kN>
+bool route_overlaps(iq_dtype_t dtype, int64_t tokens, int64_t width, int32_t top_k,
+                    int32_t experts, const int32_t* position, const int32_t* offsets,
+                    const float* weights, const float* weights_grad, const Rows (&tensors)[kN])
+{
+    const int64_t n = tokens * top_k;
+    iqk::Region out[2], in[kN + 2];
+    for (int i = 0; i < kN; ++i) {
+        const Rows& t = tensors[i];
+        (i < kN - 1 ? in[i] : out[0]) =
+            region(t.p, t.sorted ? n : tokens, width, t.ld, value_bytes(dtype));
+    }
+    out[1] = array(weights_grad, n, 4);
+    in[kN - 1] = array(position, n, 4);
+    in[kN] = array(offsets, (int64_t)experts + 1, 4);
+    in[kN + 1] = array(weights, n, 4);
+    return overlaps(out, in);
+}
+
 }  // namespace
 
 extern "C" {
@@ -102,6 +127,9 @@ iq_status_t iq_quantize_rows(iq_dtype_t dtype, const void* x, int64_t ldx, int64
     if (!bytes || !aligned(x, bytes) || !aligned(scale, 4) || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
     if (!rows) return IQ_OK;
+    if (overlaps({region(q, rows, cols, ldq, 1), array(scale, rows, 4), array(status, 1, 4)},
+                 {region(x, rows, cols, ldx, bytes)}))
+        return IQ_ERR_ARG;
     const iq_status_t st = check_device();
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
@@ -120,6 +148,10 @@ iq_status_t iq_int8_matmul(const int8_t* x, int64_t ldx, const float* x_scale, c
     if (!bytes || !aligned(y, bytes) || !aligned(x_scale, 4) || !aligned(w_scale, 4))
         return IQ_ERR_ARG;
     if (!tokens) return IQ_OK;
+    if (overlaps({region(y, tokens, channels, ldy, bytes)},
+                 {region(x, tokens, depth, ldx, 1), array(x_scale, tokens, 4),
+                  region(w, channels, depth, ldw, 1), array(w_scale, channels, 4)}))
+        return IQ_ERR_ARG;
     int cus = 1;
     const iq_status_t st = check_device(&cus);
     if (st) return st;
@@ -151,6 +183,11 @@ iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const i
         !aligned(workspace, 16) || workspace_bytes < need || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
     if (!tokens) return IQ_OK;
+    if (overlaps({region(y, tokens, channels, ldy, bytes), array(workspace, need, 1),
+                  array(status, 1, 4)},
+                 {region(x, tokens, depth, ldx, bytes), region(w, channels, depth, ldw, 1),
+                  array(w_scale, channels, 4)}))
+        return IQ_ERR_ARG;
     int cus = 1;
     const iq_status_t st = check_device(&cus);
     if (st) return st;
@@ -188,6 +225,15 @@ iq_status_t iq_int8_expert_matmul(const int8_t* x, int64_t ldx, const float* x_s
         !aligned(order, 4) || !aligned(offsets, 4))
         return IQ_ERR_ARG;
     if (!rows) return IQ_OK;
+    const iqk::Region out = region(y, rows, channels, ldy, bytes);
+    if (overlaps({out}, {region(x, tokens, depth, ldx, 1), array(x_scale, tokens, 4),
+                         array(order, rows, 4), array(offsets, (int64_t)experts + 1, 4),
+                         array(w_scale, experts * channels, 4)}))
+        return IQ_ERR_ARG;
+    // The weights as a whole first: only where that meets the output, each of them.
+    if (overlap(out, array(w, (experts - 1) * w_stride + (channels - 1) * ldw + depth, 1)))
+        for (int32_t e = 0; e < experts; ++e)
+            if (overlap(out, region(w + e * w_stride, channels, depth, ldw, 1))) return IQ_ERR_ARG;
     int cus = 1;
     const iq_status_t st = check_device(&cus);
     if (st) return st;
@@ -218,12 +264,16 @@ iq_status_t iq_expert_sort(const void* choice, int32_t choice_bytes, int64_t tok
         !aligned(order, 4) || !aligned(position, 4) || !aligned(offsets, 4) ||
         !aligned(workspace, 4) || workspace_bytes < need || (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
+    const int64_t n = tokens * top_k;
+    if (overlaps({array(order, n, 4), array(position, n, 4), array(offsets, (int64_t)experts + 1, 4),
+                  array(workspace, need, 1), array(status, 1, 4)},
+                 {array(choice, n, choice_bytes)}))
+        return IQ_ERR_ARG;
     const iq_status_t st = check_device();
     if (st) return st;
     return run_with_status(status, stream, [&](int32_t* s) {
-        return iqk::launch_expert_sort(choice, choice_bytes, tokens * top_k, experts, order,
-                                       position, offsets, static_cast<int32_t*>(workspace), s,
-                                       stream);
+        return iqk::launch_expert_sort(choice, choice_bytes, n, experts, order, position, offsets,
+                                       static_cast<int32_t*>(workspace), s, stream);
     });
 }
 
@@ -232,9 +282,12 @@ iq_status_t iq_expert_dispatch(iq_dtype_t dtype, const void* x, int64_t ldx, int
                                const int32_t* offsets, int32_t experts, void* sorted, int64_t lds,
                                hipStream_t stream)
 {
-    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets,
-                                {{x, ldx, false, false}, {sorted, lds, true, true}});
+    const Rows tensors[] = {{x, ldx, false, false}, {sorted, lds, true, true}};
+    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets, tensors);
     if (st || !tokens) return st;
+    if (route_overlaps(dtype, tokens, width, top_k, experts, position, offsets, nullptr, nullptr,
+                       tensors))
+        return IQ_ERR_ARG;
     st = check_device();
     if (st) return st;
     const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
@@ -246,9 +299,12 @@ iq_status_t iq_expert_dispatch_backward(iq_dtype_t dtype, const void* sorted_gra
                                         int32_t top_k, const int32_t* offsets, int32_t experts,
                                         void* x_grad, int64_t ldx, hipStream_t stream)
 {
-    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets,
-                                {{sorted_grad, lds, true, false}, {x_grad, ldx, false, true}});
+    const Rows tensors[] = {{sorted_grad, lds, true, false}, {x_grad, ldx, false, true}};
+    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets, tensors);
     if (st || !tokens) return st;
+    if (route_overlaps(dtype, tokens, width, top_k, experts, position, offsets, nullptr, nullptr,
+                       tensors))
+        return IQ_ERR_ARG;
     st = check_device();
     if (st) return st;
     const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
@@ -261,12 +317,15 @@ iq_status_t iq_expert_combine(iq_dtype_t dtype, const void* y, int64_t ldy, int6
                               const int32_t* offsets, int32_t experts, const float* weights,
                               void* out, int64_t ldo, hipStream_t stream)
 {
-    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets,
-                                {{y, ldy, true, false}, {out, ldo, false, true}});
+    const Rows tensors[] = {{y, ldy, true, false}, {out, ldo, false, true}};
+    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets, tensors);
     if (st) return st;
     if (tokens && !weights) return IQ_ERR_NULL;
     if (!aligned(weights, 4)) return IQ_ERR_ARG;
     if (!tokens) return IQ_OK;
+    if (route_overlaps(dtype, tokens, width, top_k, experts, position, offsets, weights, nullptr,
+                       tensors))
+        return IQ_ERR_ARG;
     st = check_device();
     if (st) return st;
     const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);
@@ -280,13 +339,16 @@ iq_status_t iq_expert_combine_backward(iq_dtype_t dtype, const void* out_grad, i
                                        const float* weights, void* y_grad, int64_t ldg,
                                        float* weights_grad, hipStream_t stream)
 {
-    iq_status_t st = route_args(
-        dtype, tokens, width, top_k, experts, position, offsets,
-        {{out_grad, ldo, false, false}, {y, ldy, true, false}, {y_grad, ldg, true, true}});
+    const Rows tensors[] = {{out_grad, ldo, false, false}, {y, ldy, true, false},
+                            {y_grad, ldg, true, true}};
+    iq_status_t st = route_args(dtype, tokens, width, top_k, experts, position, offsets, tensors);
     if (st) return st;
     if (tokens && (!weights || !weights_grad)) return IQ_ERR_NULL;
     if (!aligned(weights, 4) || !aligned(weights_grad, 4)) return IQ_ERR_ARG;
     if (!tokens) return IQ_OK;
+    if (route_overlaps(dtype, tokens, width, top_k, experts, position, offsets, weights,
+                       weights_grad, tensors))
+        return IQ_ERR_ARG;
     st = check_device();
     if (st) return st;
     const iqk::Route r = route(dtype, tokens, width, position, top_k, offsets, experts);

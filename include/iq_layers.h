@@ -18,7 +18,8 @@
  *     only; rows that start on 16 bytes are read fastest.
  *   - An empty batch (no tokens) is no error: the call writes what is left to
  *     write (the offsets of iq_expert_sort) and returns IQ_OK.
- *   - Outputs may not overlap inputs (not checked).
+ *   - Outputs and workspaces may not overlap inputs or each other (IQ_ERR_ARG).
+ *     Rows may interleave: column slices of one buffer do not overlap.
  */
 #ifndef IQ_LAYERS_H
 #define IQ_LAYERS_H
