@@ -194,7 +194,14 @@ struct Result {
             value_error("out must be [" + std::to_string(rows) + ", " + std::to_string(cols) + "]");
         ld = m.ld;
     }
-    void* data() const { return t.data_ptr(); }
+    // For the call that writes it: a tensor of the caller's is a new version of
+    // itself from then on, which autograd checks what it has saved by.  (Inference
+    // tensors have no versions.)
+    void* data() const
+    {
+        if (given && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        return t.data_ptr();
+    }
     PyObject* object() const
     {
         if (!given) return THPVariable_Wrap(t);

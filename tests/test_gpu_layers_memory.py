@@ -66,3 +66,45 @@ def test_overlapping_results_are_refused(tokens):
         with pytest.raises(iq.IQError) as e:
             call()
         assert e.value.name == "IQ_ERR_ARG"
+
+
+def calls_with_out(tokens=6):
+    """(call taking out=, a fitting out) of every operator that takes one."""
+    w, ws = iq.quantize_rows(normal((64, 64), 1))
+    x = normal((tokens, 64), 2, torch.bfloat16)
+    q, s = iq.quantize_rows(x)
+    p = torch.arange(tokens, dtype=torch.int32, device=DEV)[:, None]
+    f = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    one = torch.ones((tokens, 1), device=DEV)
+    return [(call, torch.zeros((tokens, 64), dtype=torch.bfloat16, device=DEV)) for call in (
+        lambda out: iq.int8_linear(x, w, ws, out=out), lambda out: iq.int8_matmul(q, s, w, ws, out=out),
+        lambda out: iq.int8_expert_matmul(q, s, w[None], ws[None], f, out=out),
+        lambda out: iq.expert_dispatch(x, p, f, out=out),
+        lambda out: iq.expert_dispatch_backward(x, p, f, out=out),
+        lambda out: iq.expert_combine(x, p, f, one, out=out))]
+
+
+def test_writing_a_result_makes_a_new_version():
+    for call, out in calls_with_out():
+        before = out._version
+        assert call(out) is out and out._version > before
+    # a tensor that a graph has saved and that was written over since is noticed
+    for call, out in calls_with_out():
+        leaf = torch.ones((6, 64), device=DEV, requires_grad=True)
+        product = leaf * out.float().mul_(1.0)               # saves a copy: not affected
+        call(out)
+        product.sum().backward()
+        loss = (leaf.bfloat16() * out).sum()                 # saves out itself
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+
+def test_writing_results_in_inference_mode():
+    with torch.inference_mode():
+        for call, out in calls_with_out():
+            assert out.is_inference() and call(out) is out and out.any()
+    for call, out in calls_with_out():
+        with torch.inference_mode():
+            held = torch.zeros_like(out)
+        assert call(held) is held and held.any()
