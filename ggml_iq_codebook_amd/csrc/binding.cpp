@@ -5,11 +5,12 @@
 // host: an operator on a few tokens runs for 3 to 6 us, and checking its
 // tensors and allocating its result took 5 us from Python and takes 1.5 us
 // here (a launch is 2.7 us).  The functions are positional; layers.py gives
-// them names, defaults and documentation.
+// them names, defaults, documentation and their place in autograd's graph.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -467,7 +468,18 @@ PyObject* expert_combine_backward(PyObject* const* a)
 
 PyObject* iq_error = nullptr;         // the package's exception class
 
-template <PyObject* (*kCall)(PyObject* const*), int kArgs>
+// Whether autograd records what is done with these arguments.
+bool recorded(PyObject* const* args, Py_ssize_t count)
+{
+    if (!at::GradMode::is_enabled()) return false;
+    for (Py_ssize_t i = 0; i < count; ++i)
+        if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
+    return false;
+}
+
+// kGraph: results can be part of a graph.  A call that autograd records answers
+// NotImplemented, and layers.py makes it again from a function of the graph.
+template <PyObject* (*kCall)(PyObject* const*), int kArgs, bool kGraph>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count)
 {
     HANDLE_TH_ERRORS
@@ -475,6 +487,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count)
         PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", kArgs, count);
         return nullptr;
     }
+    if (kGraph && recorded(args, count)) Py_RETURN_NOTIMPLEMENTED;
     try {
         return kCall(args);
     } catch (const Refused& r) {
@@ -497,23 +510,23 @@ PyObject* set_error(PyObject*, PyObject* type)
     Py_RETURN_NONE;
 }
 
-template <PyObject* (*kCall)(PyObject* const*), int kArgs>
+template <PyObject* (*kCall)(PyObject* const*), int kArgs, bool kGraph>
 PyMethodDef method(const char* name)
 {
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<kCall, kArgs>)),
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<kCall, kArgs, kGraph>)),
             METH_FASTCALL, nullptr};
 }
 
 PyMethodDef methods[] = {
-    method<quantize_rows, 2>("quantize_rows"),
-    method<int8_matmul, 6>("int8_matmul"),
-    method<int8_linear, 5>("int8_linear"),
-    method<int8_expert_matmul, 9>("int8_expert_matmul"),
-    method<expert_sort, 3>("expert_sort"),
-    method<expert_dispatch, 4>("expert_dispatch"),
-    method<expert_dispatch_backward, 4>("expert_dispatch_backward"),
-    method<expert_combine, 5>("expert_combine"),
-    method<expert_combine_backward, 5>("expert_combine_backward"),
+    method<quantize_rows, 2, false>("quantize_rows"),
+    method<int8_matmul, 6, true>("int8_matmul"),
+    method<int8_linear, 5, true>("int8_linear"),
+    method<int8_expert_matmul, 9, true>("int8_expert_matmul"),
+    method<expert_sort, 3, false>("expert_sort"),
+    method<expert_dispatch, 4, true>("expert_dispatch"),
+    method<expert_dispatch_backward, 4, true>("expert_dispatch_backward"),
+    method<expert_combine, 5, true>("expert_combine"),
+    method<expert_combine_backward, 5, true>("expert_combine_backward"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -9,6 +9,12 @@ stream.  That part is compiled (``csrc/binding.cpp``): the small calls of these
 operators are bound by the host.  Matrices are two-dimensional with consecutive
 values in a row; rows may have a stride of their own (slices of larger tensors
 are taken as they are).  All tensors are on the current device.
+
+Autograd: ``expert_dispatch``, its gradient and ``expert_combine`` are functions
+of the graph like torch's own.  The 8-bit products and ``expert_combine_backward``
+have no gradient: a backward pass that reaches their results raises.
+``quantize_rows`` and ``expert_sort`` answer with integers and scales of them,
+which are constants.  ``out`` cannot be given where gradients are recorded.
 """
 
 from __future__ import annotations
@@ -19,6 +25,7 @@ import os
 import sys
 
 import torch
+from torch.autograd import Function
 
 # The package, whose helpers and loaded library the calls below use (it imports
 # this module before it defines them).
@@ -73,6 +80,67 @@ def _word(status, check, like):
     return status
 
 
+# --- autograd: what the calls below turn to when the binding answers
+# NotImplemented, because gradients are being recorded for one of the arguments
+
+def _rows(grad):
+    """A gradient as the kernels take it: consecutive values in a row."""
+    return grad if grad.stride(1) == 1 else grad.contiguous()
+
+
+class _Dispatch(Function):
+    @staticmethod
+    def forward(ctx, x, position, offsets):
+        ctx.save_for_backward(position, offsets)
+        return _binding.expert_dispatch(x, position, offsets, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return expert_dispatch_backward(_rows(grad), *ctx.saved_tensors), None, None
+
+
+class _DispatchBackward(Function):
+    @staticmethod
+    def forward(ctx, grad, position, offsets):
+        ctx.save_for_backward(position, offsets)
+        return _binding.expert_dispatch_backward(grad, position, offsets, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return expert_dispatch(_rows(grad), *ctx.saved_tensors), None, None
+
+
+class _Combine(Function):
+    @staticmethod
+    def forward(ctx, y, position, offsets, weights):
+        ctx.save_for_backward(y, position, offsets, weights)
+        return _binding.expert_combine(y, position, offsets, weights, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        y_grad, weights_grad = expert_combine_backward(_rows(grad), *ctx.saved_tensors)
+        return y_grad, None, None, weights_grad
+
+
+class _NoGradient(Function):
+    """A call whose results have a place in the graph, but no gradient beyond."""
+
+    @staticmethod
+    def forward(ctx, name, *args):
+        ctx.name = name
+        return getattr(_binding, name)(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("%s has no gradient; call it under torch.no_grad() or on detached tensors"
+                           % ctx.name)
+
+
+def _no_out(out):
+    if out is not None:
+        raise ValueError("out cannot be given where gradients are recorded")
+
+
 def quantize_rows(x, *, status=None, check=True):
     """Rows of ``x`` [rows, cols] (fp32, bf16 or fp16) as 8-bit integers with a scale each.
 
@@ -80,7 +148,8 @@ def quantize_rows(x, *, status=None, check=True):
     scale = max|row| * (1/127) and code = the integer nearest to value / scale
     (halves to even).  A weight's rows are its output channels, so this also
     makes the weight of the products below.  A row with a NaN or an infinity is
-    reported (IQ_ERR_NONFINITE) and written as zeros.
+    reported (IQ_ERR_NONFINITE) and written as zeros.  Autograd takes both results
+    as constants.
     """
     status = _word(status, check, x)
     result = (_binding or _native()).quantize_rows(x, status)
@@ -96,7 +165,12 @@ def int8_matmul(x, x_scale, w, w_scale, *, dtype=torch.bfloat16, out=None):
     ``quantize_rows`` gives them).  The sums are exact.  Returns
     [tokens, channels] in ``dtype`` (or in the type of ``out``).
     """
-    return (_binding or _native()).int8_matmul(x, x_scale, w, w_scale, dtype, out)
+    args = x, x_scale, w, w_scale, dtype, out
+    result = (_binding or _native()).int8_matmul(*args)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _NoGradient.apply("int8_matmul", *args)
+    return result
 
 
 def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
@@ -107,7 +181,11 @@ def int8_linear(x, w, w_scale, *, out=None, status=None, check=True):
     (IQ_ERR_NONFINITE) and answered with zeros.
     """
     status = _word(status, check, x)
-    result = (_binding or _native()).int8_linear(x, w, w_scale, out, status)
+    args = x, w, w_scale, out, status
+    result = (_binding or _native()).int8_linear(*args)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _NoGradient.apply("int8_linear", *args)
     iq._raise_on_status(status, check, "iq_int8_linear")
     return result
 
@@ -123,8 +201,12 @@ def int8_expert_matmul(x, x_scale, w, w_scale, offsets, order=None, *, top_k=1,
     ``order`` it is row p of ``x`` (already dispatched).  Rows of dropped
     choices are zeros.
     """
-    return (_binding or _native()).int8_expert_matmul(x, x_scale, w, w_scale, offsets, order, top_k,
-                                                      dtype, out)
+    args = x, x_scale, w, w_scale, offsets, order, top_k, dtype, out
+    result = (_binding or _native()).int8_expert_matmul(*args)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _NoGradient.apply("int8_expert_matmul", *args)
+    return result
 
 
 def expert_sort(experts_of, num_experts, *, status=None, check=True):
@@ -146,22 +228,38 @@ def expert_sort(experts_of, num_experts, *, status=None, check=True):
 def expert_dispatch(x, position, offsets, *, out=None):
     """Tokens copied to the places of their choices: [tokens * top_k, width],
     row position[t, j] holding ``x[t]`` (zeros where the choice was dropped)."""
-    return (_binding or _native()).expert_dispatch(x, position, offsets, out)
+    result = (_binding or _native()).expert_dispatch(x, position, offsets, out)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _Dispatch.apply(x, position, offsets)
+    return result
 
 
 def expert_dispatch_backward(grad, position, offsets, *, out=None):
     """The gradient of ``expert_dispatch``: for the gradient of its result, that
     of ``x``, the sum over each token's kept choices."""
-    return (_binding or _native()).expert_dispatch_backward(grad, position, offsets, out)
+    result = (_binding or _native()).expert_dispatch_backward(grad, position, offsets, out)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _DispatchBackward.apply(grad, position, offsets)
+    return result
 
 
 def expert_combine(y, position, offsets, weights, *, out=None):
     """Rows brought back to their tokens: out[t] = the sum over the kept choices
     j of weights[t, j] * y[position[t, j]] (``weights`` fp32 [tokens, top_k])."""
-    return (_binding or _native()).expert_combine(y, position, offsets, weights, out)
+    result = (_binding or _native()).expert_combine(y, position, offsets, weights, out)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _Combine.apply(y, position, offsets, weights)
+    return result
 
 
 def expert_combine_backward(grad, y, position, offsets, weights):
     """The gradients of ``expert_combine`` for the gradient ``grad`` [tokens,
     width] of its result: (that of ``y``, that of ``weights``)."""
-    return (_binding or _native()).expert_combine_backward(grad, y, position, offsets, weights)
+    args = grad, y, position, offsets, weights
+    result = (_binding or _native()).expert_combine_backward(*args)
+    if result is NotImplemented:
+        result = _NoGradient.apply("expert_combine_backward", *args)
+    return result
