@@ -17,7 +17,7 @@ import os
 
 import torch  # noqa: F401  (device memory and streams; loads the HIP runtime first)
 
-from . import layers as _layers
+from . import layers
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libiqcodec.so")
@@ -84,7 +84,7 @@ def load(build_if_missing: bool = True):
     L.iq_choice_search.restype = ctypes.c_int
     L.iq_choice_search_blocks.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P]
     L.iq_choice_search_blocks.restype = ctypes.c_int
-    _layers.declare(L)
+    layers.declare(L)
     _lib = L
     return L
 
