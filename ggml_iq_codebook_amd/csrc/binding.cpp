@@ -68,6 +68,8 @@ const at::Tensor& gpu_tensor(PyObject* o, const char* name)
     if (!THPVariable_Check(o)) type_error(std::string(name) + " must be a torch.Tensor");
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) value_error(std::string(name) + " must be on the GPU");
+    // Its memory holds the values with the other sign.
+    if (t.is_neg()) value_error(std::string(name) + " is a negated view: call resolve_neg() on it");
     return t;
 }
 

@@ -108,3 +108,14 @@ def test_writing_results_in_inference_mode():
         with torch.inference_mode():
             held = torch.zeros_like(out)
         assert call(held) is held and held.any()
+
+
+def test_negated_views_are_refused():
+    """The imaginary part of a conjugate is a view of the values with the other sign."""
+    z = torch.complex(normal((12, 1), 1), normal((12, 1), 2))
+    x = z.conj().imag
+    assert x.is_neg()
+    with pytest.raises(ValueError, match="resolve_neg"):
+        iq.quantize_rows(x)
+    q, _ = iq.quantize_rows(x.resolve_neg())
+    assert torch.equal(q.float(), 127 * torch.sign(-z.imag))
