@@ -259,7 +259,7 @@ __device__ __forceinline__ void wait_and_meet()
 // unit loads from the L2 (about 38 bytes a clock), so small products take many
 // small tiles: 24 x 1536 x 4096 in a graph 4.3 us with 16 x 16 tiles, 6.1 with
 // 32 x 32.  Products by expert of few rows are bound by HBM (16 tokens, 2 of 16
-// experts of 1536 x 4096: 16 us, 6.2 TB/s).
+// experts of 1536 x 4096: 95 MB read in 18 us, 5.3 TB/s).
 template <int kRows, int kChannels, int kWT, int kWC, int kWK, int kDepth, int kStages,
           bool kPingPong, bool kDirect, bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWK* kWave, kWT* kWC* kWK / 4) void int8_tile_kernel(

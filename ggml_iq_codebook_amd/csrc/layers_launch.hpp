@@ -52,8 +52,9 @@ __host__ __device__ constexpr int decode_stride(int depth)
 }
 // Where one launch pays: its rounding is repeated by every workgroup, so its cost
 // goes with the parts and with the rounds of workgroups on the 256 compute
-// units.  GPU time, one launch against two, us (as calls of their own the second
-// launch adds 3 more):
+// units of a whole card (not the device's own: the rule also sizes the workspace,
+// which has to be the same wherever it is asked).  GPU time, one launch against
+// two, us (as calls of their own the second launch adds 3 more):
 //   channels x depth, tokens   1            2            4            8
 //   1024 x 1024                3.6 / 6.0                              5.0 / 6.4
 //   4096 x 4096                7.8 / 10.0   8.8 / 9.8   10.5 / 9.9

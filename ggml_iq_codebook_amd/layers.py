@@ -10,6 +10,10 @@ operators are bound by the host.  Matrices are two-dimensional with consecutive
 values in a row; rows may have a stride of their own (slices of larger tensors
 are taken as they are).  All tensors are on the current device.
 
+Calls that may find a data error wait for the GPU and raise it (``check=True``).
+With a status word of the caller's and ``check=False`` nothing waits, and the word
+can be read later; without a word ``check=False`` clears one that nobody reads.
+
 Autograd: ``expert_dispatch``, its gradient and ``expert_combine`` are functions
 of the graph like torch's own.  The 8-bit products and ``expert_combine_backward``
 have no gradient: a backward pass that reaches their results raises.

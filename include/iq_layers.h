@@ -69,7 +69,9 @@ iq_status_t iq_int8_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const i
  * as zeros.  The token of row p is order[p] / top_k (iq_expert_sort's order of
  * the choices), or p itself where order is NULL (x already in that order;
  * tokens >= rows).  w_scale is [experts][channels].  `order` and `offsets` are
- * read on the device: values out of range are clamped into it. */
+ * read on the device: values out of range are clamped into it; a row that no
+ * expert's range holds (offsets that begin after 0 or decrease, which
+ * iq_expert_sort does not give) is not written. */
 iq_status_t iq_int8_expert_matmul(const int8_t* x, int64_t ldx, const float* x_scale,
                                   int64_t tokens, const int32_t* order, int32_t top_k,
                                   const int32_t* offsets, int32_t experts, int64_t rows,
@@ -96,7 +98,8 @@ iq_status_t iq_expert_sort(const void* choice, int32_t choice_bytes, int64_t tok
 /* Tokens copied to the places of their choices: sorted[position[t][j]] = x[t],
  * zeros where the choice was dropped (position >= offsets[experts]).  x is
  * [tokens][width], sorted [tokens*top_k][width].  `position` is read on the
- * device: places outside 0..tokens*top_k-1 are skipped, here and below. */
+ * device: places outside 0..tokens*top_k-1 are skipped, here and below, and
+ * sorted rows that are no choice's place are not written. */
 iq_status_t iq_expert_dispatch(iq_dtype_t dtype, const void* x, int64_t ldx, int64_t tokens,
                                int64_t width, const int32_t* position, int32_t top_k,
                                const int32_t* offsets, int32_t experts, void* sorted, int64_t lds,
