@@ -6,39 +6,23 @@
 
 #include "api_common.hpp"
 #include "iq_layers.h"
+#include "layers_args.hpp"
 #include "layers_launch.hpp"
 #include "overlap.hpp"
 
 using iqk::aligned;
 using iqk::array;
+using iqk::bad_choices;
+using iqk::bad_rows;
 using iqk::check_device;
 using iqk::from_hip;
 using iqk::overlaps;
 using iqk::region;
+using iqk::round_up;
 using iqk::run_with_status;
+using iqk::value_bytes;
 
 namespace {
-
-// Bytes per value, 0 for a type these calls do not take.
-int value_bytes(iq_dtype_t t)
-{
-    return t == IQ_DTYPE_F32 ? 4 : (t == IQ_DTYPE_BF16 || t == IQ_DTYPE_F16 ? 2 : 0);
-}
-
-// Rows of `cols` values with stride ld: every offset stays below 2^61.
-// Outputs may not have rows that overlap (ld >= cols); inputs may.
-bool bad_rows(int64_t rows, int64_t cols, int64_t ld, bool output)
-{
-    if (rows < 0 || cols < 1 || ld < 0 || (output && rows > 1 && ld < cols)) return true;
-    const int64_t most = INT64_C(1) << 61;
-    return cols > most || (ld > 0 && rows > most / ld);
-}
-
-// Places are 32-bit.
-bool bad_choices(int64_t tokens, int32_t top_k)
-{
-    return tokens < 0 || top_k < 1 || tokens > INT32_MAX / top_k;
-}
 
 bool bad_product(int64_t tokens, int64_t channels, int64_t depth, int64_t ldx, int64_t ldw,
                  int64_t ldy, int64_t rows)
@@ -47,8 +31,6 @@ bool bad_product(int64_t tokens, int64_t channels, int64_t depth, int64_t ldx, i
            tokens > INT32_MAX || rows > INT32_MAX || bad_rows(tokens, depth, ldx, false) ||
            bad_rows(channels, depth, ldw, false) || bad_rows(rows, channels, ldy, true);
 }
-
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The codes of iq_int8_linear: rows that start on 16 bytes.
 int64_t code_stride(int64_t depth) { return round_up(depth, 16); }
