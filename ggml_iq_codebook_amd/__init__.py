@@ -1,7 +1,8 @@
 """Python binding of libiqcodec.so: MI355X-native importance-weighted IQ1_S /
 IQ2_XS codebook-search encode, decode, candidate emission and local-Hessian
 choice search; and the layer operators of ``layers.py``: products in 8-bit
-integers, dense and by expert, and the routing of tokens to experts.
+integers and with 4-bit weights, dense and by expert, the router, and the routing
+of tokens to experts.
 
 This module only marshals arguments: it checks tensors, takes their device
 pointers and the current HIP stream from PyTorch, and calls the C-ABI declared
@@ -371,5 +372,7 @@ def choice_search(H, cand_err, *, sweeps=2, trace=False):
 
 
 from .layers import (  # noqa: E402  (they use the helpers above)
-    expert_combine, expert_combine_backward, expert_dispatch, expert_dispatch_backward,
-    expert_sort, int8_expert_matmul, int8_linear, int8_matmul, quantize_rows)
+    dequantize_groups, expert_balance, expert_balance_backward, expert_combine,
+    expert_combine_backward, expert_dispatch, expert_dispatch_backward, expert_gate,
+    expert_gate_backward, expert_sort, fp4_expert_linear, fp4_linear, int8_expert_matmul,
+    int8_linear, int8_matmul, quantize_groups, quantize_rows)

@@ -3,7 +3,7 @@
 Every HIP source under csrc/ is compiled for gfx950 only, without packed-FP32
 instructions and without floating-point contraction (the encode's keys are
 recomputed bit-for-bit during index recovery), and linked into one shared
-library that exports the C-ABI of include/iq_codec.h and include/iq_layers.h.
+library that exports the C-ABI declared in include/.
 csrc/binding.cpp, host code only, becomes the extension module of the layer
 operators' binding.
 """

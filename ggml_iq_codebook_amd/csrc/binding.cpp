@@ -1,5 +1,5 @@
-// binding.cpp -- the Python binding of include/iq_layers.h: checks tensors,
-// allocates the results that were not given and calls the C-ABI.
+// binding.cpp -- the Python binding of include/iq_layers.h, iq_fp4.h and iq_router.h:
+// checks tensors, allocates the results that were not given and calls the C-ABI.
 //
 // It is compiled because the small calls of these operators are bound by the
 // host: an operator on a few tokens runs for 3 to 6 us, and checking its
@@ -18,7 +18,9 @@
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "iq_fp4.h"
 #include "iq_layers.h"
+#include "iq_router.h"
 
 namespace {
 
@@ -37,6 +39,7 @@ std::string name_of(at::ScalarType t)
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
     case at::kChar: return "torch.int8";
+    case at::kByte: return "torch.uint8";
     default: return std::string("torch.") + c10::toString(t);
     }
 }
@@ -151,6 +154,37 @@ Matrix codes(const Call& c, PyObject* o, const char* name)
     const at::Tensor& t = tensor(c, o, name);
     expect_type(t, at::kChar, name);
     return Matrix(t, name);
+}
+
+// Codes and scales of `groups` 4-bit groups of 32 to a row: bytes, `per_group` of
+// them for each group.
+Matrix group_bytes(const Call& c, PyObject* o, const char* name, int64_t per_group, int64_t groups)
+{
+    const at::Tensor& t = tensor(c, o, name);
+    expect_type(t, at::kByte, name);
+    const Matrix m(t, name);
+    if (m.cols != per_group * groups)
+        value_error(std::string(name) + " must have " + std::to_string(per_group * groups) + " columns");
+    return m;
+}
+
+// A depth in groups.
+int64_t groups_of(int64_t values, const char* name)
+{
+    if (values < IQ_GROUP || values % IQ_GROUP)
+        value_error(std::string(name) + " must have a multiple of " + std::to_string(IQ_GROUP) + " columns");
+    return values / IQ_GROUP;
+}
+
+// The same for each expert: [experts, channels, bytes] with consecutive bytes.
+const at::Tensor& expert_bytes(const Call& c, PyObject* o, const char* name, int64_t bytes)
+{
+    const at::Tensor& t = tensor(c, o, name);
+    expect_type(t, at::kByte, name);
+    if (t.dim() != 3 || t.size(2) != bytes || (t.stride(2) != 1 && bytes != 1))
+        value_error(std::string(name) + " must be [experts, channels, " + std::to_string(bytes) +
+                    "] with consecutive bytes in a row");
+    return t;
 }
 
 // A contiguous tensor of that type and shape.
@@ -365,6 +399,206 @@ PyObject* int8_expert_matmul(PyObject* const* a)
     return y.object();
 }
 
+PyObject* quantize_groups(PyObject* const* a)
+{
+    const Call c(a[0], "w");
+    iq_dtype_t type;
+    const Matrix w = values(c, a[0], "w", &type);
+    const int64_t groups = groups_of(w.cols, "w");
+    int32_t* status = status_word(c, a[1]);
+    at::Tensor codes = at::empty({w.rows, w.cols / 2}, c.options(at::kByte));
+    at::Tensor scale = at::empty({w.rows, groups}, c.options(at::kByte));
+    check(unlocked([&] {
+        return iq_quantize_groups(type, w.data(), w.ld, w.rows, w.cols,
+                                  static_cast<uint8_t*>(codes.data_ptr()), w.cols / 2,
+                                  static_cast<uint8_t*>(scale.data_ptr()), groups, status, c.stream);
+    }), "iq_quantize_groups");
+    return tuple({codes, scale});
+}
+
+PyObject* dequantize_groups(PyObject* const* a)
+{
+    const Call c(a[0], "codes");
+    const at::Tensor& t = tensor(c, a[0], "codes");
+    expect_type(t, at::kByte, "codes");
+    const Matrix codes(t, "codes");
+    const int64_t groups = groups_of(2 * codes.cols, "the values of codes");
+    const Matrix scale = group_bytes(c, a[1], "scale", 1, groups);
+    expect_rows(scale, codes.rows, "scale");
+    iq_dtype_t type;
+    const at::ScalarType out = result_type(a[2], a[3], &type);
+    const Result y(c, a[3], codes.rows, 2 * codes.cols, out);
+    check(unlocked([&] {
+        return iq_dequantize_groups(static_cast<uint8_t*>(codes.data()), codes.ld,
+                                    static_cast<uint8_t*>(scale.data()), scale.ld, codes.rows,
+                                    2 * codes.cols, type, y.data(), y.ld, c.stream);
+    }), "iq_dequantize_groups");
+    return y.object();
+}
+
+PyObject* fp4_linear(PyObject* const* a)
+{
+    const Call c(a[0], "x");
+    iq_dtype_t type;
+    const Matrix x = values(c, a[0], "x", &type);
+    const int64_t groups = groups_of(x.cols, "x");
+    const Matrix w = group_bytes(c, a[1], "w", IQ_GROUP / 2, groups);
+    const Matrix scale = group_bytes(c, a[2], "w_scale", 1, groups);
+    expect_rows(scale, w.rows, "w_scale");
+    const Result y(c, a[3], x.rows, w.rows, x.t.scalar_type());
+    const int64_t need = iq_fp4_linear_workspace(type, x.data(), x.ld, x.rows, w.rows, x.cols);
+    at::Tensor work;
+    if (need) work = at::empty({need}, c.options(at::kByte));
+    check(unlocked([&] {
+        return iq_fp4_linear(type, x.data(), x.ld, static_cast<uint8_t*>(w.data()), w.ld,
+                             static_cast<uint8_t*>(scale.data()), scale.ld, x.rows, w.rows, x.cols,
+                             y.data(), y.ld, need ? work.data_ptr() : nullptr, need, c.stream);
+    }), "iq_fp4_linear");
+    return y.object();
+}
+
+PyObject* fp4_expert_linear(PyObject* const* a)
+{
+    const Call c(a[0], "x");
+    iq_dtype_t type;
+    const Matrix x = values(c, a[0], "x", &type);
+    const int64_t groups = groups_of(x.cols, "x");
+    const at::Tensor& w = expert_bytes(c, a[1], "w", IQ_GROUP / 2 * groups);
+    const at::Tensor& scale = expert_bytes(c, a[2], "w_scale", groups);
+    const int64_t experts = w.size(0), channels = w.size(1);
+    if (scale.size(0) != experts || scale.size(1) != channels)
+        value_error("w_scale must be [" + std::to_string(experts) + ", " + std::to_string(channels) +
+                    ", " + std::to_string(groups) + "]");
+    const int32_t top_k = int32_of(a[5], "top_k");
+    const int32_t* offsets = array<int32_t>(c, a[3], "offsets", at::kInt, {experts + 1});
+    int64_t rows = x.rows;
+    const int32_t* order = nullptr;
+    if (a[4] != Py_None) {
+        rows = x.rows * std::max(top_k, 0);
+        order = array<int32_t>(c, a[4], "order", at::kInt, {rows});
+    }
+    const Result y(c, a[6], rows, channels, x.t.scalar_type());
+    if (experts > INT32_MAX) value_error("too many experts");
+    const int64_t need = iq_fp4_expert_linear_workspace(type, x.data(), x.ld, x.rows,
+                                                        (int32_t)experts, rows, channels, x.cols);
+    at::Tensor work;
+    if (need) work = at::empty({need}, c.options(at::kByte));
+    check(unlocked([&] {
+        return iq_fp4_expert_linear(type, x.data(), x.ld, x.rows, order, top_k, offsets,
+                                    (int32_t)experts, rows, static_cast<uint8_t*>(w.data_ptr()),
+                                    w.stride(1), w.stride(0),
+                                    static_cast<uint8_t*>(scale.data_ptr()), scale.stride(1),
+                                    scale.stride(0), channels, x.cols, y.data(), y.ld,
+                                    need ? work.data_ptr() : nullptr, need, c.stream);
+    }), "iq_fp4_expert_linear");
+    return y.object();
+}
+
+// [tokens, experts].
+Matrix logits_of(const Call& c, PyObject* o, iq_dtype_t* type)
+{
+    const Matrix l = values(c, o, "logits", type);
+    if (l.cols > INT32_MAX) value_error("too many experts");
+    return l;
+}
+
+bool bool_of(PyObject* o, const char* name)
+{
+    if (!PyBool_Check(o)) type_error(std::string(name) + " must be True or False");
+    return o == Py_True;
+}
+
+PyObject* expert_gate(PyObject* const* a)
+{
+    const Call c(a[0], "logits");
+    iq_dtype_t type;
+    const Matrix l = logits_of(c, a[0], &type);
+    const int32_t top_k = int32_of(a[1], "top_k");
+    const bool renormalize = bool_of(a[2], "renormalize");
+    int32_t* status = status_word(c, a[3]);
+    const int64_t k = std::max(top_k, 0);
+    at::Tensor choice = at::empty({l.rows, k}, c.options(at::kInt));
+    at::Tensor weights = at::empty({l.rows, k}, c.options(at::kFloat));
+    check(unlocked([&] {
+        return iq_expert_gate(type, l.data(), l.ld, l.rows, (int32_t)l.cols, top_k, renormalize,
+                              static_cast<int32_t*>(choice.data_ptr()),
+                              static_cast<float*>(weights.data_ptr()), status, c.stream);
+    }), "iq_expert_gate");
+    return tuple({choice, weights});
+}
+
+PyObject* expert_gate_backward(PyObject* const* a)
+{
+    const Call c(a[0], "grad");
+    iq_dtype_t type;
+    const Matrix l = logits_of(c, a[1], &type);
+    const at::Tensor& t = tensor(c, a[2], "choice");
+    if (t.dim() != 2 || t.size(0) != l.rows)
+        value_error("choice must be a contiguous [tokens, top_k] tensor");
+    const int64_t k = t.size(1);
+    if (k > INT32_MAX) value_error("too many choices");
+    const int32_t* choice = array<int32_t>(c, a[2], "choice", at::kInt, {l.rows, k});
+    const float* weights = array<float>(c, a[3], "weights", at::kFloat, {l.rows, k});
+    const float* grad = array<float>(c, a[0], "grad", at::kFloat, {l.rows, k});
+    const bool renormalize = bool_of(a[4], "renormalize");
+    at::Tensor out = at::empty({l.rows, l.cols}, c.options(l.t.scalar_type()));
+    check(unlocked([&] {
+        return iq_expert_gate_backward(type, grad, l.data(), l.ld, l.rows, (int32_t)l.cols, choice,
+                                       weights, (int32_t)k, renormalize, out.data_ptr(), l.cols,
+                                       c.stream);
+    }), "iq_expert_gate_backward");
+    return THPVariable_Wrap(out);
+}
+
+PyObject* expert_balance(PyObject* const* a)
+{
+    const Call c(a[0], "logits");
+    iq_dtype_t type;
+    const Matrix l = logits_of(c, a[0], &type);
+    const at::Tensor& choice = tensor(c, a[1], "choice");
+    if (choice.scalar_type() != at::kInt && choice.scalar_type() != at::kLong)
+        type_error("choice must be int32 or int64, got " + name_of(choice.scalar_type()));
+    if (choice.dim() != 2 || choice.size(0) != l.rows || !choice.is_contiguous())
+        value_error("choice must be a contiguous [tokens, top_k] tensor");
+    const int64_t k = choice.size(1);
+    if (k > INT32_MAX) value_error("too many choices");
+    int32_t* status = status_word(c, a[2]);
+    at::Tensor loss = at::empty({}, c.options(at::kFloat));
+    at::Tensor counts = at::empty({l.cols}, c.options(at::kInt));
+    at::Tensor live = at::empty({}, c.options(at::kInt));
+    const int64_t need = iq_expert_balance_workspace(l.rows, (int32_t)l.cols);
+    at::Tensor work;
+    if (need) work = at::empty({need}, c.options(at::kByte));
+    check(unlocked([&] {
+        return iq_expert_balance(type, l.data(), l.ld, l.rows, (int32_t)l.cols, choice.data_ptr(),
+                                 (int32_t)choice.element_size(), (int32_t)k,
+                                 static_cast<float*>(loss.data_ptr()),
+                                 static_cast<int32_t*>(counts.data_ptr()),
+                                 static_cast<int32_t*>(live.data_ptr()),
+                                 need ? work.data_ptr() : nullptr, need, status, c.stream);
+    }), "iq_expert_balance");
+    return tuple({loss, counts, live});
+}
+
+PyObject* expert_balance_backward(PyObject* const* a)
+{
+    const Call c(a[0], "grad");
+    iq_dtype_t type;
+    const Matrix l = logits_of(c, a[1], &type);
+    const at::Tensor& grad = tensor(c, a[0], "grad");
+    expect_type(grad, at::kFloat, "grad");
+    if (grad.numel() != 1) value_error("grad must have one value");
+    const int32_t* counts = array<int32_t>(c, a[2], "counts", at::kInt, {l.cols});
+    const int32_t* live = array<int32_t>(c, a[3], "live", at::kInt, {});
+    at::Tensor out = at::empty({l.rows, l.cols}, c.options(l.t.scalar_type()));
+    check(unlocked([&] {
+        return iq_expert_balance_backward(type, static_cast<float*>(grad.data_ptr()), l.data(), l.ld,
+                                          l.rows, (int32_t)l.cols, counts, live, out.data_ptr(),
+                                          l.cols, c.stream);
+    }), "iq_expert_balance_backward");
+    return THPVariable_Wrap(out);
+}
+
 PyObject* expert_sort(PyObject* const* a)
 {
     const Call c(a[0], "experts_of");
@@ -524,6 +758,14 @@ PyMethodDef methods[] = {
     method<int8_matmul, 6, true>("int8_matmul"),
     method<int8_linear, 5, true>("int8_linear"),
     method<int8_expert_matmul, 9, true>("int8_expert_matmul"),
+    method<quantize_groups, 2, false>("quantize_groups"),
+    method<dequantize_groups, 4, false>("dequantize_groups"),
+    method<fp4_linear, 4, true>("fp4_linear"),
+    method<fp4_expert_linear, 7, true>("fp4_expert_linear"),
+    method<expert_gate, 4, true>("expert_gate"),
+    method<expert_gate_backward, 5, true>("expert_gate_backward"),
+    method<expert_balance, 3, true>("expert_balance"),
+    method<expert_balance_backward, 4, true>("expert_balance_backward"),
     method<expert_sort, 3, false>("expert_sort"),
     method<expert_dispatch, 4, true>("expert_dispatch"),
     method<expert_dispatch_backward, 4, true>("expert_dispatch_backward"),

@@ -1,0 +1,32 @@
+// fp4_common.hpp -- 4-bit floats in groups of 32 that share a power of two.
+//
+// A code is a sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6 (bits: sign, two of
+// exponent, one of mantissa); byte i of a row holds the codes of values 2i (low)
+// and 2i + 1.  A group's scale byte s stands for 2^(s - 127), 255 for NaN.  The
+// conversion instructions of gfx950 take the scale as a float of which they use
+// the exponent: the byte shifted to its place.  Their results were compared with
+// this definition for every code and every scale byte: exact in bf16 (subnormal
+// where they are below 2^-126, infinite from 2^128 on, NaN for the byte 255).
+#pragma once
+
+#include "iq_fp4.h"
+#include "layers_common.hpp"
+
+namespace iqk {
+
+constexpr int kGroup = IQ_GROUP;
+
+__device__ __forceinline__ float group_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// The 8 codes of a word as bf16, in order.
+__device__ __forceinline__ v8bf values_of(uint32_t codes, float scale)
+{
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2),
+                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3)};
+    return __builtin_bit_cast(v8bf, v);
+}
+
+}  // namespace iqk

@@ -72,6 +72,63 @@ inline bool int8_decode_takes(int64_t tokens, int64_t channels, int64_t depth)
 hipError_t launch_int8_decode(const Int8Product& p, int dtype, const void* x, int64_t ldx,
                               int32_t* status, hipStream_t stream);
 
+// Rows as 4-bit floats in groups of 32, and back.
+hipError_t launch_quantize_groups(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                                  uint8_t* codes, int64_t ldc, uint8_t* scale, int64_t lds,
+                                  int32_t* status, hipStream_t stream);
+hipError_t launch_dequantize_groups(const uint8_t* codes, int64_t ldc, const uint8_t* scale,
+                                    int64_t lds, int64_t rows, int64_t cols, int dtype, void* y,
+                                    int64_t ldy, hipStream_t stream);
+
+// A product with such a weight, dense or by expert as an Int8Product is.
+struct Fp4Product {
+    const void* x;            // of the type of y
+    int64_t ldx;
+    const uint8_t* w;
+    int64_t ldw;              // bytes, like the strides below
+    int64_t w_stride;         // from one expert's weight to the next
+    const uint8_t* scale;
+    int64_t lds;
+    int64_t s_stride;
+    void* y;
+    int64_t ldy;
+    int64_t tokens;
+    int64_t rows;
+    int channels;
+    int depth;
+    int dtype;
+    const int32_t* order;
+    const int32_t* offsets;
+    int experts;
+    int top_k;
+    int64_t first_tile = 0;   // of the launch's part of the tiles
+};
+int64_t fp4_workspace(int dtype, const void* x, int64_t ldx, int64_t tokens, int64_t rows,
+                      int experts, int64_t channels, int64_t depth);
+hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, int cus, hipStream_t stream);
+
+// The router: rows of logits.
+struct Logits {
+    const void* p;
+    int64_t ld;
+    int64_t tokens;
+    int experts;
+    int dtype;
+};
+hipError_t launch_expert_gate(const Logits& l, int top_k, bool renormalize, int32_t* choice,
+                              float* weights, int32_t* status, hipStream_t stream);
+hipError_t launch_expert_gate_backward(const Logits& l, const float* weights_grad,
+                                       const int32_t* choice, const float* weights, int top_k,
+                                       bool renormalize, void* grad, int64_t ldg,
+                                       hipStream_t stream);
+int64_t balance_workspace(int64_t tokens, int experts);
+hipError_t launch_expert_balance(const Logits& l, const void* choice, int choice_bytes, int top_k,
+                                 float* loss, int32_t* counts, int32_t* live, void* workspace,
+                                 int32_t* status, hipStream_t stream);
+hipError_t launch_expert_balance_backward(const Logits& l, const float* loss_grad,
+                                          const int32_t* counts, const int32_t* live, void* grad,
+                                          int64_t ldg, hipStream_t stream);
+
 // Routing.  chunks: how many workgroups share the sort of n choices.
 struct SortPlan {
     int chunks;

@@ -1,7 +1,8 @@
-"""Python binding of the layer operators of libiqcodec.so (``include/iq_layers.h``):
-products in 8-bit integers with a scale per token and per channel, dense and
-with a weight per expert, and the routing of tokens to experts and back with
-its gradients.
+"""Python binding of the layer operators of libiqcodec.so (``include/iq_layers.h``,
+``iq_fp4.h``, ``iq_router.h``):
+products in 8-bit integers with a scale per token and per channel and products
+with 4-bit weights, dense and with a weight per expert, the router with its
+balance loss, and the routing of tokens to experts and back, with gradients.
 
 Like the rest of the binding it only marshals: tensors are checked, results
 that were not given are allocated, and the library is called on the current HIP
@@ -14,11 +15,12 @@ Calls that may find a data error wait for the GPU and raise it (``check=True``).
 With a status word of the caller's and ``check=False`` nothing waits, and the word
 can be read later; without a word ``check=False`` clears one that nobody reads.
 
-Autograd: ``expert_dispatch``, its gradient and ``expert_combine`` are functions
-of the graph like torch's own.  The 8-bit products and ``expert_combine_backward``
-have no gradient: a backward pass that reaches their results raises.
-``quantize_rows`` and ``expert_sort`` answer with integers and scales of them,
-which are constants.  ``out`` cannot be given where gradients are recorded.
+Autograd: ``expert_gate``, ``expert_balance``, ``expert_dispatch``, its gradient and
+``expert_combine`` are functions of the graph like torch's own.  The products and
+the other gradients have no gradient: a backward pass that reaches their results
+raises.  ``quantize_rows``, ``quantize_groups`` and ``expert_sort`` answer with
+integers and scales of them, which are constants.  ``out`` cannot be given where
+gradients are recorded.
 """
 
 from __future__ import annotations
@@ -53,7 +55,8 @@ def _native():
 
 
 def declare(L):
-    """Argument types of the entry points of ``include/iq_layers.h``."""
+    """Argument types of the entry points of ``include/iq_layers.h``, ``iq_fp4.h`` and
+    ``iq_router.h``."""
     P, i64, i32, c = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
     for name, args in {
         "iq_quantize_rows": [c, P, i64, i64, i64, P, i64, P, P, P],
@@ -61,6 +64,15 @@ def declare(L):
         "iq_int8_linear": [c, P, i64, P, i64, P, i64, i64, i64, P, i64, P, i64, P, P],
         "iq_int8_expert_matmul": [P, i64, P, i64, P, i32, P, i32, i64, P, i64, i64, P, i64, i64,
                                   c, P, i64, P],
+        "iq_quantize_groups": [c, P, i64, i64, i64, P, i64, P, i64, P, P],
+        "iq_dequantize_groups": [P, i64, P, i64, i64, i64, c, P, i64, P],
+        "iq_fp4_linear": [c, P, i64, P, i64, P, i64, i64, i64, i64, P, i64, P, i64, P],
+        "iq_fp4_expert_linear": [c, P, i64, i64, P, i32, P, i32, i64, P, i64, i64, P, i64, i64, i64,
+                                 i64, P, i64, P, i64, P],
+        "iq_expert_gate": [c, P, i64, i64, i32, i32, i32, P, P, P, P],
+        "iq_expert_gate_backward": [c, P, P, i64, i64, i32, P, P, i32, i32, P, i64, P],
+        "iq_expert_balance": [c, P, i64, i64, i32, P, i32, i32, P, P, P, P, i64, P, P],
+        "iq_expert_balance_backward": [c, P, P, i64, i64, i32, P, P, P, i64, P],
         "iq_expert_sort": [P, i32, i64, i32, i32, P, P, P, P, i64, P, P],
         "iq_expert_dispatch": [c, P, i64, i64, i64, P, i32, P, i32, P, i64, P],
         "iq_expert_dispatch_backward": [c, P, i64, i64, i64, P, i32, P, i32, P, i64, P],
@@ -71,6 +83,9 @@ def declare(L):
         f = getattr(L, name)
         f.argtypes, f.restype = args, c
     for name, args in {"iq_int8_linear_workspace": [i64, i64, i64],
+                       "iq_fp4_linear_workspace": [c, P, i64, i64, i64, i64],
+                       "iq_fp4_expert_linear_workspace": [c, P, i64, i64, i32, i64, i64, i64],
+                       "iq_expert_balance_workspace": [i64, i32],
                        "iq_expert_sort_workspace": [i64, i32]}.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, i64
@@ -124,6 +139,34 @@ class _Combine(Function):
     def backward(ctx, grad):
         y_grad, weights_grad = expert_combine_backward(_rows(grad), *ctx.saved_tensors)
         return y_grad, None, None, weights_grad
+
+
+class _Gate(Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, renormalize, status):
+        choice, weights = _binding.expert_gate(logits, top_k, renormalize, status)
+        ctx.mark_non_differentiable(choice)
+        ctx.save_for_backward(logits, choice, weights)
+        ctx.renormalize = renormalize
+        return choice, weights
+
+    @staticmethod
+    def backward(ctx, _, grad):
+        return expert_gate_backward(grad.contiguous(), *ctx.saved_tensors,
+                                    renormalize=ctx.renormalize), None, None, None
+
+
+class _Balance(Function):
+    @staticmethod
+    def forward(ctx, logits, choice, status):
+        loss, counts, live = _binding.expert_balance(logits, choice, status)
+        ctx.mark_non_differentiable(counts, live)
+        ctx.save_for_backward(logits, counts, live)
+        return loss, counts, live
+
+    @staticmethod
+    def backward(ctx, grad, *_):
+        return expert_balance_backward(grad, *ctx.saved_tensors), None, None
 
 
 class _NoGradient(Function):
@@ -210,6 +253,122 @@ def int8_expert_matmul(x, x_scale, w, w_scale, offsets, order=None, *, top_k=1,
     if result is NotImplemented:
         _no_out(out)
         result = _NoGradient.apply("int8_expert_matmul", *args)
+    return result
+
+
+def quantize_groups(w, *, status=None, check=True):
+    """Rows of ``w`` [rows, cols] (fp32, bf16 or fp16, cols a multiple of 32) as 4-bit
+    floats, 32 of which share a power of two (the MXFP4 format).
+
+    Returns (codes uint8 [rows, cols / 2], scale uint8 [rows, cols / 32]): the
+    scale byte s of a group stands for 2^(s - 127), a quarter of the power of two
+    at or below the group's largest magnitude, and a code for a sign and one of 0, 1/2,
+    1, 3/2, 2, 3, 4, 6, the nearest to value / scale (halves to the even code, 6
+    beyond 6); a byte has two codes, the first one in its low bits.  A group with a
+    NaN or an infinity is reported (IQ_ERR_NONFINITE) and written as zeros.
+    Autograd takes both results as constants.
+    """
+    status = _word(status, check, w)
+    result = (_binding or _native()).quantize_groups(w, status)
+    iq._raise_on_status(status, check, "iq_quantize_groups")
+    return result
+
+
+def dequantize_groups(codes, scale, *, dtype=torch.float32, out=None):
+    """What ``quantize_groups`` wrote, as values in ``dtype`` (or in the type of ``out``):
+    [rows, cols].  They are exact in fp32 and bf16, rounded in fp16."""
+    return (_binding or _native()).dequantize_groups(codes, scale, dtype, out)
+
+
+def fp4_linear(x, w, w_scale, *, out=None):
+    """``x @ values(w, w_scale).T`` with a 4-bit weight as ``quantize_groups`` gives it.
+
+    ``x`` [tokens, depth] in fp32, bf16 or fp16; ``w`` uint8 [channels, depth / 2] and
+    ``w_scale`` uint8 [channels, depth / 32].  The products are exact, the sums in
+    fp32; the result [tokens, channels] has the type of ``x``.  A NaN or an
+    infinity in ``x`` passes to its token's results.
+    """
+    args = x, w, w_scale, out
+    result = (_binding or _native()).fp4_linear(*args)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _NoGradient.apply("fp4_linear", *args)
+    return result
+
+
+def fp4_expert_linear(x, w, w_scale, offsets, order=None, *, top_k=1, out=None):
+    """``fp4_linear`` with a weight per expert, on rows in the order of their experts.
+
+    ``w`` uint8 [experts, channels, depth / 2] and ``w_scale`` uint8 [experts, channels,
+    depth / 32]; ``offsets`` and ``order`` as for ``int8_expert_matmul``.
+    """
+    args = x, w, w_scale, offsets, order, top_k, out
+    result = (_binding or _native()).fp4_expert_linear(*args)
+    if result is NotImplemented:
+        _no_out(out)
+        result = _NoGradient.apply("fp4_expert_linear", *args)
+    return result
+
+
+def expert_gate(logits, top_k, *, renormalize=True, status=None, check=True):
+    """The router's choice: each token's ``top_k`` experts and their weights.
+
+    ``logits`` [tokens, experts] in fp32, bf16 or fp16.  Returns (choice int32 [tokens,
+    top_k], weights fp32 [tokens, top_k]): the largest logits' experts, the largest
+    first and the lowest expert first among equal ones, with their probabilities
+    (softmax over all experts), which ``renormalize`` divides by their sum.  A logit
+    of -inf is an expert that is never chosen; where fewer than ``top_k`` are left,
+    as for a padded token with nothing but -inf, the last choices are -1 with weight
+    0 (``expert_sort`` takes them as dropped).  A token with a NaN or +inf is reported
+    (IQ_ERR_NONFINITE) and has no choices.  The weights have a gradient.
+    """
+    status = _word(status, check, logits)
+    args = logits, top_k, renormalize, status
+    result = (_binding or _native()).expert_gate(*args)
+    if result is NotImplemented:
+        result = _Gate.apply(*args)
+    iq._raise_on_status(status, check, "iq_expert_gate")
+    return result
+
+
+def expert_gate_backward(grad, logits, choice, weights, *, renormalize=True):
+    """The gradient of ``expert_gate``: of ``logits``, for the gradient ``grad`` fp32
+    [tokens, top_k] of its weights."""
+    args = grad, logits, choice, weights, renormalize
+    result = (_binding or _native()).expert_gate_backward(*args)
+    if result is NotImplemented:
+        result = _NoGradient.apply("expert_gate_backward", *args)
+    return result
+
+
+def expert_balance(logits, choice, *, status=None, check=True):
+    """How evenly the experts are used: (loss, counts, live).
+
+    ``logits`` [tokens, experts], ``choice`` [tokens, top_k] int32 or int64, -1 where a
+    choice was dropped.  ``counts`` int32 [experts] are the choices of each expert,
+    ``live`` the number of tokens with a finite logit (padded tokens have none), and
+    the loss, a scalar, experts * sum_e (counts[e] / sum(counts)) * (mean over the live
+    tokens of expert e's probability): 1 where either is even.  It has a gradient;
+    the counts are constants.  A token with a NaN or +inf is reported
+    (IQ_ERR_NONFINITE) and does not count, nor does a choice out of range
+    (IQ_ERR_INDEX).
+    """
+    status = _word(status, check, logits)
+    args = logits, choice, status
+    result = (_binding or _native()).expert_balance(*args)
+    if result is NotImplemented:
+        result = _Balance.apply(*args)
+    iq._raise_on_status(status, check, "iq_expert_balance")
+    return result
+
+
+def expert_balance_backward(grad, logits, counts, live):
+    """The gradient of ``expert_balance``: of ``logits``, for the gradient ``grad`` (fp32,
+    one value) of its loss."""
+    args = grad, logits, counts, live
+    result = (_binding or _native()).expert_balance_backward(*args)
+    if result is NotImplemented:
+        result = _NoGradient.apply("expert_balance_backward", *args)
     return result
 
 
