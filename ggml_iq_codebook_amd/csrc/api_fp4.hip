@@ -126,12 +126,11 @@ iq_status_t iq_fp4_linear(iq_dtype_t dtype, const void* x, int64_t ldx, const ui
                  {region(x, tokens, depth, ldx, bytes), region(w, channels, depth / 2, ldw, 1),
                   region(w_scale, channels, depth / IQ_GROUP, lds, 1)}))
         return IQ_ERR_ARG;
-    int cus = 1;
-    const iq_status_t st = check_device(&cus);
+    const iq_status_t st = check_device();
     if (st) return st;
     const iqk::Fp4Product p = {x, ldx, w, ldw, 0, w_scale, lds, 0, y, ldy, tokens, tokens,
                                (int)channels, (int)depth, (int)dtype, nullptr, nullptr, 0, 1};
-    return from_hip(iqk::launch_fp4_product(p, workspace, cus, stream));
+    return from_hip(iqk::launch_fp4_product(p, workspace, stream));
 }
 
 int64_t iq_fp4_expert_linear_workspace(iq_dtype_t dtype, const void* x, int64_t ldx,
@@ -173,13 +172,12 @@ iq_status_t iq_fp4_expert_linear(iq_dtype_t dtype, const void* x, int64_t ldx, i
         if (meets(o, w, experts, w_stride, channels, depth / 2, ldw) ||
             meets(o, w_scale, experts, s_stride, channels, depth / IQ_GROUP, lds))
             return IQ_ERR_ARG;
-    int cus = 1;
-    const iq_status_t st = check_device(&cus);
+    const iq_status_t st = check_device();
     if (st) return st;
     const iqk::Fp4Product p = {x, ldx, w, ldw, w_stride, w_scale, lds, s_stride, y, ldy, tokens,
                                rows, (int)channels, (int)depth, (int)dtype, order, offsets,
                                experts, top_k};
-    return from_hip(iqk::launch_fp4_product(p, workspace, cus, stream));
+    return from_hip(iqk::launch_fp4_product(p, workspace, stream));
 }
 
 }  // extern "C"

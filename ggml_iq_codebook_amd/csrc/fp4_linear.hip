@@ -15,17 +15,28 @@
 #include "expert_tiles.hpp"
 #include "fp4_common.hpp"
 #include "layers_launch.hpp"
+#include "row_codes.hpp"
 
 namespace iqk {
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kPiece = 128;           // depth of a step: four groups, 64 bytes of codes a row
 
 __device__ __forceinline__ v4f mfma16(v8bf a, v8bf b, v4f c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// 16 bytes at any alignment.
+__device__ __forceinline__ v4u load16(const uint8_t* from)
+{
+    v4u v;
+    __builtin_memcpy(&v, from, 16);
+    return v;
 }
 
 // bf16 parts that a type is split into.
@@ -42,34 +53,54 @@ __device__ __forceinline__ void split_values(const typename Value<kDT>::raw (&r)
         part[0] = __builtin_bit_cast(v8bf, r);
     } else {
         constexpr int kN = kSplit<kDT>;
-        uint32_t u[kN][8];
+        uint32_t u[kN][8], top = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float left = Value<kDT>::load(r[i]);
-            const uint32_t bits = __float_as_uint(left);
-            const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+            top = max(top, __float_as_uint(left) & 0x7fffffffu);
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
-                u[k][i] = __float_as_uint(left) & 0xffff0000u;
-                left = left - __uint_as_float(u[k][i]);
+                u[k][i] = __float_as_uint(left);
+                left = left - __uint_as_float(u[k][i] & 0xffff0000u);
             }
-            if (!finite) {
-                u[0][i] |= bits & 0xffffu ? 0x400000u : 0u;
+        }
+        if (top >= 0x7f800000u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (finite_f32(Value<kDT>::load(r[i]))) continue;
+                // A NaN whose payload is in the bits that are cut stays one.
+                u[0][i] |= u[0][i] & 0xffffu ? 0x400000u : 0u;
 #pragma unroll
                 for (int k = 1; k < kN; ++k) u[k][i] = 0u;
             }
         }
+        // The upper halves of two words.
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = (u[k][2 * i] >> 16) | u[k][2 * i + 1];
+            for (int i = 0; i < 4; ++i)
+                w[i] = __builtin_amdgcn_perm(u[k][2 * i + 1], u[k][2 * i], 0x07060302u);
             part[k] = __builtin_bit_cast(v8bf, w);
         }
     }
 }
 
-// kN consecutive channels of one row of y, in its type.
+// The scale bytes g0 .. g0 + 15 of a row that ends before, 0 beyond its end.
+__device__ __forceinline__ v4u last_scales(const uint8_t* row, int g0, int groups)
+{
+    unsigned __int128 v = 0;
+    if (g0 >= groups) return v4u{0u, 0u, 0u, 0u};
+    if (groups >= 16) {
+        v = __builtin_bit_cast(unsigned __int128, load16(row + groups - 16)) >> 8 * (g0 + 16 - groups);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < groups - g0; ++i) v |= (unsigned __int128)row[g0 + i] << 8 * i;
+    }
+    return __builtin_bit_cast(v4u, v);
+}
+
+// 4 consecutive channels of one row of y, in its type.
 template <int kDT>
 __device__ __forceinline__ void store_channels(const Fp4Product& p, int64_t row, int channel, v4f f)
 {
@@ -98,102 +129,490 @@ __device__ __forceinline__ void store_zeros(const Fp4Product& p, const Tile& t)
     }
 }
 
-// Few rows: a workgroup takes 16 kFC channels of 16 kFT rows and its waves share
-// the depth, so both operands go straight into registers and nothing waits for
-// another wave until the sums are added at the end.  Lane l has row l % 16 of
-// both operands and group l / 16 of a step: 16 bytes of codes and 32 activations.
-template <int kDT, int kFC, int kFT, int kWaves, bool kExperts>
-__global__ __launch_bounds__(kWaves* kWave) void fp4_rows_kernel(Fp4Product p, int channel_tiles)
+// A handful of rows: a workgroup takes 16 kFC channels of kTok rows, and its waves share
+// the depth in blocks of 4 steps.  A block of the weight is asked for while the one
+// before is multiplied.  The activations, few of them, are split into their parts once
+// by the lanes together, and every lane takes its operand from there: as operands
+// straight from memory, 16 / kTok times as many would be loaded and split.
+template <int kDT, int kTok, int kFC, int kWaves, bool kExperts>
+__global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, int channel_tiles)
 {
     typedef typename Value<kDT>::raw raw;
-    constexpr int kN = kSplit<kDT>;
-    __shared__ __align__(16) v4f sums[kWaves - 1][kFC * kFT][kWave];
-    const Tile t = kExperts ? expert_tile<16 * kFT>(p, channel_tiles)
-                            : dense_tile<16 * kFT>(p, channel_tiles);
+    constexpr int kN = kSplit<kDT>, kChannels = 16 * kFC, kThreads = kWaves * kWave;
+    constexpr int kFT = (kTok + 15) / 16;
+    constexpr int kBlock = 4;
+    // Steps whose activations are staged at once, 8 values each to a lane kX times.
+    constexpr int kSub = kTok <= 2 ? 4 : (kTok == 4 ? 2 : 1);
+    constexpr int kUnits = kSub * kPiece / 8, kX = kTok * kUnits / kWave;
+    constexpr int kRow = kSub * kPiece + 8;           // rows start on different banks
+    union Shared {
+        uint16_t x[kWaves][kN][kTok][kRow];
+        float sums[kWaves][kTok][kChannels];
+    };
+    __shared__ __align__(16) Shared shared;
+    const Tile t = kExperts ? expert_tile<kTok>(p, channel_tiles) : dense_tile<kTok>(p, channel_tiles);
     if (t.expert == -2) return;
     if (t.expert == -1) {
-        store_zeros<kDT, 16 * kFT, 16 * kFC, kWaves * kWave>(p, t);
+        store_zeros<kDT, kTok, kChannels, kThreads>(p, t);
         return;
     }
     const int lane = threadIdx.x % kWave, quarter = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int channel0 = t.channel_tile * 16 * kFC;
-
-    const uint8_t *w[kFC], *scale[kFC];
-#pragma unroll
-    for (int i = 0; i < kFC; ++i) {
-        const int64_t n = min(channel0 + 16 * i + lane % 16, p.channels - 1);
-        w[i] = p.w + t.expert * p.w_stride + n * p.ldw + 16 * quarter;
-        scale[i] = p.scale + t.expert * p.s_stride + n * p.lds;
-    }
-    const raw* x[kFT];
-    bool live[kFT];
-#pragma unroll
-    for (int j = 0; j < kFT; ++j) {
-        const int64_t row = t.row0 + 16 * j + lane % 16;
-        live[j] = row < t.row_end;
-        const int64_t token = live[j] ? (kExperts ? token_of(p, row) : row) : 0;
-        x[j] = static_cast<const raw*>(p.x) + token * p.ldx + kGroup * quarter;
-    }
-
+    const int channel0 = t.channel_tile * kChannels;
     const int groups = p.depth / kGroup;
     const int steps = (groups + 3) / 4;
     const int first = (int)((int64_t)steps * wave / kWaves);
     const int last = (int)((int64_t)steps * (wave + 1) / kWaves);
-    v4f acc[kFC][kFT] = {};
-    for (int s = first; s < last; ++s) {
-        const int group = 4 * s + quarter;
-        const bool there = group < groups;
-        uint4 codes[kFC];
-        float power[kFC];
+
+    // Beyond the last group, whose activations are zeros: its codes, with scale 0.
+    const uint8_t *w[kFC], *scale[kFC];
+#pragma unroll
+    for (int i = 0; i < kFC; ++i) {
+        const int64_t n = min(channel0 + 16 * i + lane % 16, p.channels - 1);
+        w[i] = p.w + t.expert * p.w_stride + n * p.ldw;
+        scale[i] = p.scale + t.expert * p.s_stride + n * p.lds;
+    }
+    v4u codes[2][kBlock][kFC], scales[2][kFC];
+    auto fetch = [&](int b, int s) {
 #pragma unroll
         for (int i = 0; i < kFC; ++i) {
-            codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (there) __builtin_memcpy(&codes[i], w[i] + (int64_t)s * (kPiece / 2), 16);
-            power[i] = group_scale(scale[i][min(group, groups - 1)]);
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j)
+                if (s + j < last)
+                    codes[b][j][i] = load16(w[i] + min(4 * (s + j) + quarter, groups - 1) * (kGroup / 2));
+            if (s < last)
+                scales[b][i] = 4 * s + 16 <= groups ? load16(scale[i] + 4 * s)
+                                                    : last_scales(scale[i], 4 * s, groups);
         }
+    };
+    fetch(0, first);
+
+    const raw* from[kX];
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+        const int64_t row = min(t.row0 + (i * kWave + lane) / kUnits, t.row_end - 1);
+        from[i] = static_cast<const raw*>(p.x) + (kExperts ? token_of(p, row) : row) * p.ldx;
+    }
+    Chunk<kDT, true> held[kX];
+    auto fetch_x = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+            const int at = s * kPiece + (i * kWave + lane) % kUnits * 8;
+            held[i].load(from[i], at, p.depth);
+        }
+    };
+    auto stage_x = [&]() {
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+            const int unit = i * kWave + lane;
+            v8bf part[kN];
+            raw r[8];
+            __builtin_memcpy(r, held[i].r, sizeof(r));
+            split_values<kDT>(r, part);
+#pragma unroll
+            for (int q = 0; q < kN; ++q)
+                *reinterpret_cast<v8bf*>(&shared.x[wave][q][unit / kUnits][unit % kUnits * 8]) = part[q];
+        }
+    };
+    v4f acc[kFC][kFT] = {};
+    auto multiply = [&](int in_sub, const v4u (&word)[kFC], const v4u (&scales_of)[kFC], int j) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             v8bf b[kFT][kN];
 #pragma unroll
-            for (int j = 0; j < kFT; ++j) {
-                raw r[8] = {};
-                if (there && live[j])
-                    __builtin_memcpy(r, x[j] + (int64_t)s * kPiece + 8 * k, sizeof(r));
-                split_values<kDT>(r, b[j]);
-            }
+            for (int f = 0; f < kFT; ++f)
+#pragma unroll
+                for (int q = 0; q < kN; ++q)
+                    b[f][q] = *reinterpret_cast<const v8bf*>(
+                        &shared.x[wave][q][(16 * f + lane % 16) % kTok]
+                                 [in_sub * kPiece + 32 * quarter + 8 * k]);
 #pragma unroll
             for (int i = 0; i < kFC; ++i) {
-                const uint32_t word = k == 0 ? codes[i].x : k == 1 ? codes[i].y
-                                    : k == 2 ? codes[i].z : codes[i].w;
-                const v8bf a = values_of(word, power[i]);
+                const v8bf a = values_of(word[i][k], group_scale(scales_of[i][j] >> 8 * quarter & 0xffu));
 #pragma unroll
-                for (int j = 0; j < kFT; ++j)
+                for (int f = 0; f < kFT; ++f)
 #pragma unroll
-                    for (int q = kN - 1; q >= 0; --q) acc[i][j] = mfma16(a, b[j][q], acc[i][j]);
+                    for (int q = kN - 1; q >= 0; --q) acc[i][f] = mfma16(a, b[f][q], acc[i][f]);
+            }
+        }
+    };
+    if (first < last) fetch_x(first);
+    for (int s0 = first; s0 < last; s0 += 2 * kBlock) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s1 = s0 + h * kBlock;
+            if (s1 >= last) break;
+            fetch(1 - h, s1 + kBlock);
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                const int s = s1 + j;
+                if (s >= last) break;
+                if (j % kSub == 0) {
+                    stage_x();
+                    if (s + kSub < last) fetch_x(s + kSub);
+                }
+                multiply(j % kSub, codes[h][j], scales[h], j);
             }
         }
     }
-    if (wave) {
+
+    __syncthreads();
+    if (lane % 16 < kTok) {
 #pragma unroll
         for (int i = 0; i < kFC; ++i)
 #pragma unroll
-            for (int j = 0; j < kFT; ++j) sums[wave - 1][i * kFT + j][lane] = acc[i][j];
+            for (int f = 0; f < kFT; ++f)
+                *reinterpret_cast<v4f*>(&shared.sums[wave][16 * f + lane % 16][16 * i + 4 * quarter]) =
+                    acc[i][f];
     }
     __syncthreads();
-    if (wave) return;
+    for (int i = threadIdx.x; i < kTok * kChannels; i += kThreads) {
+        const int64_t row = t.row0 + i / kChannels;
+        const int channel = channel0 + i % kChannels;
+        if (row >= t.row_end || channel >= p.channels) continue;
+        float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kFC; ++i)
-#pragma unroll
-        for (int j = 0; j < kFT; ++j) {
-            v4f sum = acc[i][j];
-#pragma unroll
-            for (int v = 0; v < kWaves - 1; ++v) sum += sums[v][i * kFT + j][lane];
-            const int64_t row = t.row0 + 16 * j + lane % 16;
-            const int channel = channel0 + 16 * i + 4 * quarter;
-            if (row < t.row_end && channel < p.channels) store_channels<kDT>(p, row, channel, sum);
-        }
+        for (int v = 0; v < kWaves; ++v) sum += shared.sums[v][i / kChannels][i % kChannels];
+        static_cast<raw*>(p.y)[row * p.ldy + channel] = Value<kDT>::store(sum);
+    }
 }
+
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void global_void;
+
+// 16 bytes a lane from global memory into LDS at `to` + 16 * lane.
+__device__ __forceinline__ void copy_to_lds(const uint16_t* from, uint16_t* to)
+{
+    __builtin_amdgcn_global_load_lds((global_void*)(uintptr_t)from, (lds_void*)to, 16, 0, 0);
+}
+
+// The same from base + offset + step bytes, with the offset of the lane's own; zeros where
+// it is kBeyond.  (The host's pass over this file does not know the type of a buffer.)
+constexpr uint32_t kBeyond = 0xffffffffu;
+__device__ __forceinline__ void copy_to_lds(const uint16_t* base, uint32_t offset, int step,
+                                            uint16_t* to)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(base), 0, kBeyond - 1, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (lds_void*)to, 16, offset, step, 0, 0);
+#endif
+}
+
+// Waits until at most kLeft of this wave's loads are under way and all its LDS
+// reads have arrived, then for the other waves.  The wait is the compiler's own
+// instruction, so that it knows which registers have their values.
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet()
+{
+    static_assert(kLeft < 64, "vmcnt holds 6 bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((kLeft & 15) | 7 << 4 | (kLeft >> 4) << 14);
+    asm volatile("s_barrier" ::: "memory");
+}
+
+__device__ const uint16_t kZeros[8] __attribute__((aligned(16))) = {};
+
+// x as bf16 parts, those of each piece one after another, in rows of ldx values
+// that start on 16 bytes and have `width` of them: bf16 activations as they are where
+// they do (one part), others as split_kernel lays them out.
+struct Parts {
+    const uint16_t* x;
+    int64_t ldx;
+    int width;
+};
+
+// kWT x kWC waves share a tile of kRows rows of y by kChannels channels, each a
+// part of kRows/kWT by kChannels/kWC, in steps of 128 of the depth.  The activations
+// go through a ring of kStages buffers in LDS that direct copies fill kStages - 1
+// steps ahead.  The weight comes in chunks of kChunk steps, through registers into
+// two buffers of codes (any alignment, whole cache lines of its rows), its scales 8
+// steps at a time, and becomes bf16 where it is multiplied, four instructions for 8
+// values.
+//
+// The second half of the waves runs half a step behind (ping-pong): on each SIMD one
+// wave multiplies while the other reads its operands.  A step is two barriers long.
+template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
+          bool kExperts>
+__global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel(Fp4Product p,
+                                                                               Parts parts,
+                                                                               int channel_tiles)
+{
+    typedef typename Value<kDT>::raw raw;
+    constexpr int kWaves = kWT * kWC, kThreads = kWaves * kWave;
+    constexpr int kFT = kRows / kWT / 16, kFC = kChannels / kWC / 16;
+    constexpr int kParts = kSplit<kDT>;
+    constexpr int kRowsPerLoad = 4;   // of 256 bytes each
+    constexpr int kLoads = kRows / kRowsPerLoad / kWaves;
+    // Groups of a chunk, 16 bytes of codes each, and a thread's part of them.
+    constexpr int kGroups = 4 * kChunk, kCodes = kChannels * kGroups / kThreads;
+    // Scales come for more steps at once, 16 groups to a thread: what they cost is the
+    // cache lines they are spread over.
+    constexpr int kScales = 32, kScaleThreads = kChannels * kScales / 16;
+    constexpr int kScaleRow = kScales / 4 + 1;        // words: rows start on different banks
+    static_assert(kLoads * kRowsPerLoad * kWaves == kRows && kFT > 0 && kFC > 0 &&
+                  kCodes * kThreads == kChannels * kGroups && kScaleThreads <= kThreads, "tile");
+    struct Staged {
+        uint16_t x[kStages][kRows * kPiece];
+        v4u codes[2][kChannels * kGroups];
+        uint32_t scales[2][kChannels * kScaleRow];
+    };
+    __shared__ __align__(1024) Staged staged;
+
+    const Tile t = kExperts ? expert_tile<kRows>(p, channel_tiles)
+                            : dense_tile<kRows>(p, channel_tiles);
+    if (t.expert == -2) return;
+    if (t.expert == -1) {
+        store_zeros<kDT, kRows, kChannels, kThreads>(p, t);
+        return;
+    }
+    const int lane = threadIdx.x % kWave, quarter = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wt = wave % kWT, wc = wave / kWT;
+
+    // Staged rows in pieces of 16 bytes, piece c in slot c ^ (row % 16): 16 lanes that
+    // read one piece of consecutive rows meet different banks.  Rows beyond the last
+    // repeat it: their results are not stored.
+    auto column = [&](int i) {
+        return ((lane % 16) ^ ((wave * kLoads + i) * kRowsPerLoad + lane / 16) % 16) * 8;
+    };
+    // Dense rows by 32-bit offsets into a buffer that begins at the tile's first row,
+    // where an offset beyond its end reads zeros; gathered rows by addresses.
+    const uint16_t* from[kExperts ? kLoads : 1];
+    uint32_t near[kExperts ? 1 : kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = (wave * kLoads + i) * kRowsPerLoad + lane / 16;
+        const int64_t row = min(t.row0 + r, t.row_end - 1);
+        if constexpr (kExperts)
+            from[i] = parts.x + token_of(p, row) * parts.ldx + column(i);
+        else
+            near[i] = ((uint32_t)(row - t.row0) * (uint32_t)parts.ldx + column(i)) * 2;
+    }
+    const uint16_t* x0 = parts.x + (kExperts ? 0 : t.row0 * parts.ldx);
+    // Steps beyond the last are zeros.
+    auto fetch = [&](int b, int step) {
+        const int at = step * kPiece;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const bool here = at + column(i) < parts.width;
+            uint16_t* to = &staged.x[b][(wave * kLoads + i) * 512];
+            if constexpr (kExperts)
+                copy_to_lds(here ? from[i] + at : kZeros, to);
+            else
+                copy_to_lds(x0, here ? near[i] : kBeyond, at * 2, to);
+        }
+    };
+
+    const int groups = p.depth / kGroup;
+    const int channel0 = t.channel_tile * kChannels;
+    const uint8_t* w = p.w + t.expert * p.w_stride + (int64_t)channel0 * p.ldw;
+    const uint8_t* scale = p.scale + t.expert * p.s_stride + (int64_t)channel0 * p.lds;
+    // Row r's group g of a chunk in slot g ^ slot(r).
+    auto slot = [](int r) { return kGroups == 8 ? r % 8 : r / 2 % kGroups; };
+    v4u codes[kCodes];
+    auto fetch_codes = [&](int chunk) {
+#pragma unroll
+        for (int i = 0; i < kCodes; ++i) {
+            const int q = i * kThreads + threadIdx.x, r = q / kGroups;
+            const int n = min(r, p.channels - 1 - channel0);
+            const int g = min(chunk * kGroups + ((q % kGroups) ^ slot(r)), groups - 1);
+            codes[i] = load16(w + ((uint32_t)n * (uint32_t)p.ldw + g * (kGroup / 2)));
+        }
+    };
+    auto store_codes = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < kCodes; ++i) staged.codes[b][i * kThreads + threadIdx.x] = codes[i];
+    };
+    // Groups beyond the last, whose activations are zeros, have the smallest scale.
+    v4u scales = {};
+    auto fetch_scales = [&](int chunk) {
+        if (threadIdx.x >= kScaleThreads) return;
+        const int n = min((int)threadIdx.x / 2, p.channels - 1 - channel0);
+        const uint8_t* s = scale + (uint32_t)n * (uint32_t)p.lds;
+        const int g0 = chunk * kScales + threadIdx.x % 2 * 16;
+        if (g0 + 16 <= groups)
+            scales = load16(s + g0);
+        else
+            scales = last_scales(s, g0, groups);
+    };
+    auto store_scales = [&](int b) {
+        if (threadIdx.x >= kScaleThreads) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            staged.scales[b][threadIdx.x / 2 * kScaleRow + threadIdx.x % 2 * 4 + i] = scales[i];
+    };
+
+    v4f acc[kFC][kFT] = {};
+    v8bf x[4][kFT];
+    v4u word[kFC];
+    uint32_t byte[kFC];
+    // The ring's buffer b, and step `piece` of the weight, the one `in_chunk` of its chunk.
+    auto read = [&](int b, int piece, int in_chunk) {
+#pragma unroll
+        for (int i = 0; i < kFC; ++i) {
+            const int r = (wc * kFC + i) * 16 + lane % 16, g = 4 * in_chunk + quarter;
+            word[i] = staged.codes[piece / kChunk % 2][r * kGroups + (g ^ slot(r))];
+            byte[i] = reinterpret_cast<const uint8_t*>(
+                &staged.scales[4 * piece / kScales % 2][r * kScaleRow])[4 * piece % kScales + quarter];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < kFT; ++j) {
+                const int r = (wt * kFT + j) * 16 + lane % 16;
+                x[k][j] = *reinterpret_cast<const v8bf*>(
+                    &staged.x[b][r * kPiece + ((4 * quarter + k) ^ (lane % 16)) * 8]);
+            }
+    };
+    auto multiply = [&]() {
+        auto operand = [&](int f) {
+            return values_of(word[f % kFC][f / kFC], group_scale(byte[f % kFC]));
+        };
+        v8bf a = operand(0), next = a;
+#pragma unroll
+        for (int f = 0; f < 4 * kFC; ++f) {
+            if (f + 1 < 4 * kFC) next = operand(f + 1);
+#pragma unroll
+            for (int j = 0; j < kFT; ++j)
+                acc[f % kFC][j] = mfma16(a, x[f / kFC][j], acc[f % kFC][j]);
+            a = next;
+            // The next operand's conversions among these products.
+            constexpr int kEach = kFT >= 4 ? 1 : 4 / kFT;
+#pragma unroll
+            for (int i = 0; i < 4 / kEach; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kFT * kEach / 4, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, kEach, 0);
+            }
+        }
+    };
+
+    const int steps = (groups + 3) / 4 * kParts;
+    fetch_codes(0);
+    fetch_scales(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+    __builtin_amdgcn_sched_barrier(0);
+    store_codes(0);
+    store_scales(0);
+    fetch_scales(1);
+    fetch_codes(1);
+    constexpr int kLeft = (kStages - 2) * kLoads;
+    const bool late = wave >= kWaves / 2;
+    wait_and_meet<kLeft + kCodes>();
+    if (late) asm volatile("s_barrier" ::: "memory");
+    // A chunk of the weight is as many steps of each part of the activations.
+    constexpr int kSteps = kChunk * kParts, kTurn = kScales / kGroups;
+    int buffer = 0;
+    for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int s = s0 + u;
+            if (s >= steps) break;
+            // The chunk before, whose buffer this is, was read before the last barrier.
+            if (u == 0) {
+                store_codes((chunk + 1) % 2);
+                if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
+            }
+            read(buffer, chunk * kChunk + u / kParts, u / kParts);
+            // Into the buffer of the step before, which both halves read before the
+            // last barrier.
+            fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
+            buffer = buffer + 1 == kStages ? 0 : buffer + 1;
+            if (u == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
+                fetch_codes(chunk + 2);
+            }
+            // The next step has to be there.  The weight's codes were asked for behind the
+            // copies of step s0 + kStages - 1.
+            if (u <= kStages - 2)
+                wait_and_meet<kLeft + kCodes>();
+            else
+                wait_and_meet<kLeft>();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_barrier" ::: "memory");
+        }
+    }
+    if (!late) asm volatile("s_barrier" ::: "memory");
+
+    // Results through LDS, as the matrix instructions leave them (4 channels of a row
+    // to a lane), and out as whole rows of the wave's channels, 16 bytes a lane.
+    wait_and_meet<0>();
+    constexpr int kN = 16 / (int)sizeof(raw);
+    constexpr int kRow = kFC * 16 + kN;               // rows start on different banks
+    constexpr int kLanes = kFC * 16 / kN;             // lanes to a row
+    static_assert(kWaves * 16 * kRow * (int)sizeof(raw) <= (int)sizeof(staged), "results fit");
+    raw* mine = reinterpret_cast<raw*>(&staged) + wave * 16 * kRow;
+    const int wave_channel = channel0 + wc * kFC * 16;
+#pragma unroll
+    for (int j = 0; j < kFT; ++j) {
+        const int64_t row0 = t.row0 + (wt * kFT + j) * 16;
+#pragma unroll
+        for (int i = 0; i < kFC; ++i) {
+            raw o[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[v] = Value<kDT>::store(acc[i][j][v]);
+            __builtin_memcpy(__builtin_assume_aligned(mine + lane % 16 * kRow + i * 16 + 4 * quarter,
+                                                      4 * sizeof(raw)),
+                             o, sizeof(o));
+        }
+        // A wave's own LDS accesses are done in order.
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int s = 0; s < (16 * kLanes + kWave - 1) / kWave; ++s) {
+            const int r = (s * kWave + lane) / kLanes, c = (s * kWave + lane) % kLanes * kN;
+            const int channel = wave_channel + c;
+            if (r >= 16 || row0 + r >= t.row_end || channel >= p.channels) continue;
+            raw o[kN];
+            __builtin_memcpy(o, __builtin_assume_aligned(mine + r * kRow + c, 16), 16);
+            raw* to = static_cast<raw*>(p.y) + (row0 + r) * p.ldy + channel;
+            if (channel + kN <= p.channels) {
+                __builtin_memcpy(to, o, 16);
+            } else {
+#pragma unroll
+                for (int v = 0; v < kN; ++v)
+                    if (channel + v < p.channels) to[v] = o[v];
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Activations split into their bf16 parts, padded to whole pieces with zeros: row t,
+// piece c, part q from out[t][(c * kN + q) * 128].
+template <int kDT>
+__global__ __launch_bounds__(256) void split_kernel(const void* __restrict__ x, int64_t ldx,
+                                                    int64_t tokens, int depth, int64_t first,
+                                                    int per_row, uint16_t* __restrict__ out)
+{
+    typedef typename Value<kDT>::raw raw;
+    constexpr int kN = kSplit<kDT>;
+    const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;   // 8 values each
+    const int64_t row = i / per_row;
+    if (row >= tokens) return;
+    const int at = (int)(i - row * per_row) * 8;
+    raw r[8] = {};
+    if (at < depth)
+        __builtin_memcpy(r, static_cast<const raw*>(x) + row * ldx + at, sizeof(r));
+    v8bf part[kN];
+    split_values<kDT>(r, part);
+    uint16_t* to = out + (row * per_row * 8 + at / kPiece * kPiece) * kN + at % kPiece;
+#pragma unroll
+    for (int q = 0; q < kN; ++q) *reinterpret_cast<v8bf*>(to + q * kPiece) = part[q];
+}
+
+// Strides up to which the tile kernel's 32-bit offsets reach all of its rows.
+constexpr int64_t kNear = INT64_C(1) << 22;
 
 // Every expert (and the dropped rows) may end in a tile that is not full.
 int64_t workgroups(const Fp4Product& p, int rows, int channel_tiles)
@@ -203,17 +622,106 @@ int64_t workgroups(const Fp4Product& p, int rows, int channel_tiles)
     return row_tiles * channel_tiles;
 }
 
-template <int kDT, int kFC, int kFT, int kWaves, bool kExperts>
-hipError_t launch_rows(const Fp4Product& p, hipStream_t stream)
+// Whether the activations can be copied to LDS as they are: rows that start on 16
+// bytes, 256 of them within the reach of 32-bit offsets.
+bool direct(int dtype, const void* x, int64_t ldx, int64_t tokens)
+{
+    return dtype == IQ_DTYPE_BF16 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+           (ldx % 8 == 0 || tokens == 1) && ldx <= kNear;
+}
+
+int split_parts(int dtype) { return dtype == IQ_DTYPE_BF16 ? 1 : (dtype == IQ_DTYPE_F16 ? 2 : 3); }
+
+template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
+          bool kExperts>
+hipError_t launch_tiles(const Fp4Product& p, const Parts& parts, hipStream_t stream)
+{
+    const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
+    Fp4Product part = p;
+    return in_parts(workgroups(p, kRows, channel_tiles), kWT * kWC * kWave,
+                    [&](int64_t first, dim3 wgs) {
+        part.first_tile = first;
+        hipLaunchKernelGGL((fp4_tile_kernel<kDT, kRows, kChannels, kWT, kWC, kStages, kChunk,
+                                            kExperts>),
+                           wgs, dim3(kWT * kWC * kWave), 0, stream, part, parts, channel_tiles);
+        return hipGetLastError();
+    });
+}
+
+template <int kDT>
+hipError_t launch_split(const Fp4Product& p, void* workspace, Parts* parts, hipStream_t stream)
+{
+    const int per_row = (p.depth + kPiece - 1) / kPiece * (kPiece / 8);
+    uint16_t* out = static_cast<uint16_t*>(workspace);
+    const int width = per_row * 8 * kSplit<kDT>;
+    *parts = {out, width, width};
+    return in_parts((p.tokens * per_row + 255) / 256, 256, [&](int64_t first, dim3 wgs) {
+        hipLaunchKernelGGL(split_kernel<kDT>, wgs, dim3(256), 0, stream, p.x, p.ldx, p.tokens,
+                           p.depth, first, per_row, out);
+        return hipGetLastError();
+    });
+}
+
+template <int kDT, int kTok, int kFC, int kWaves, bool kExperts>
+hipError_t launch_few(const Fp4Product& p, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + 16 * kFC - 1) / (16 * kFC);
     Fp4Product part = p;
-    return in_parts(workgroups(p, 16 * kFT, channel_tiles), kWaves * kWave,
+    return in_parts(workgroups(p, kTok, channel_tiles), kWaves * kWave,
                     [&](int64_t first, dim3 wgs) {
         part.first_tile = first;
-        hipLaunchKernelGGL((fp4_rows_kernel<kDT, kFC, kFT, kWaves, kExperts>), wgs,
+        hipLaunchKernelGGL((fp4_few_kernel<kDT, kTok, kFC, kWaves, kExperts>), wgs,
                            dim3(kWaves * kWave), 0, stream, part, channel_tiles);
         return hipGetLastError();
+    });
+}
+
+// Whether a size, as rows * 1000 + channels, is one of the tile kernel's.
+bool is_tile(int size) { return size % 1000 >= 64; }
+
+template <int kDT, bool kExperts>
+hipError_t launch_size(int size, const Fp4Product& p, void* workspace, hipStream_t stream)
+{
+    Parts parts = {static_cast<const uint16_t*>(p.x), p.ldx, p.depth};
+    if (is_tile(size) && !direct(p.dtype, p.x, p.ldx, p.tokens)) {
+        const hipError_t e = launch_split<kDT>(p, workspace, &parts, stream);
+        if (e != hipSuccess) return e;
+    }
+    switch (size) {
+    case 1016: return launch_few<kDT, 1, 1, 8, kExperts>(p, stream);
+    case 2016: return launch_few<kDT, 2, 1, 8, kExperts>(p, stream);
+    case 4016: return launch_few<kDT, 4, 1, 8, kExperts>(p, stream);
+    case 8016: return launch_few<kDT, 8, 1, 8, kExperts>(p, stream);
+    case 16032: return launch_few<kDT, 16, 2, 8, kExperts>(p, stream);
+    // Of fp32 the parts of 32 rows leave LDS for four waves, and those of 64 no room.
+    case 32032: return launch_few<kDT, 32, 2, kDT == IQ_DTYPE_F32 ? 4 : 8, kExperts>(p, stream);
+    case 64032:
+        if constexpr (kDT == IQ_DTYPE_BF16) return launch_few<kDT, 64, 2, 8, kExperts>(p, stream);
+        break;
+    case 64064: return launch_tiles<kDT, 64, 64, 2, 2, 3, 2, kExperts>(p, parts, stream);
+    case 64128: return launch_tiles<kDT, 64, 128, 2, 4, 4, 2, kExperts>(p, parts, stream);
+    case 64256: return launch_tiles<kDT, 64, 256, 1, 8, 3, 1, kExperts>(p, parts, stream);
+    case 128128: return launch_tiles<kDT, 128, 128, 4, 2, 3, 2, kExperts>(p, parts, stream);
+    case 128256: return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, kExperts>(p, parts, stream);
+    default: break;
+    }
+    return launch_few<kDT, 16, 1, 8, kExperts>(p, stream);
+}
+
+int choose_size(int dtype, int64_t rows, int64_t channels, int64_t depth, int experts)
+{
+    if (rows > 64 && depth <= kNear / 4) return rows < 1024 ? 128128 : 128256;
+    return rows <= 1 ? 1016 : rows <= 2 ? 2016 : rows <= 4 ? 4016 : rows <= 8 ? 8016 : 16016;
+}
+
+template <bool kExperts>
+hipError_t launch_product(const Fp4Product& p, void* workspace, hipStream_t stream)
+{
+    int size = choose_size(p.dtype, p.rows, p.channels, p.depth, p.experts);
+    // Strides that 32-bit offsets do not reach: the kernel of few rows takes any.
+    if (is_tile(size) && (p.ldw > kNear || p.lds > kNear)) size = 16016;
+    return with_dtype(p.dtype, [&](auto dt) {
+        return launch_size<decltype(dt)::value, kExperts>(size, p, workspace, stream);
     });
 }
 
@@ -222,16 +730,16 @@ hipError_t launch_rows(const Fp4Product& p, hipStream_t stream)
 int64_t fp4_workspace(int dtype, const void* x, int64_t ldx, int64_t tokens, int64_t rows,
                       int experts, int64_t channels, int64_t depth)
 {
-    return 0;
+    if (!is_tile(choose_size(dtype, rows, channels, depth, experts)) ||
+        direct(dtype, x, ldx, tokens))
+        return 0;
+    return tokens * ((depth + kPiece - 1) / kPiece * kPiece) * 2 * split_parts(dtype);
 }
 
-hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, int cus, hipStream_t stream)
+hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, hipStream_t stream)
 {
-    return with_dtype(p.dtype, [&](auto dt) {
-        constexpr int kDT = decltype(dt)::value;
-        return p.experts ? launch_rows<kDT, 1, 1, 8, true>(p, stream)
-                         : launch_rows<kDT, 1, 1, 8, false>(p, stream);
-    });
+    return p.experts ? launch_product<true>(p, workspace, stream)
+                     : launch_product<false>(p, workspace, stream);
 }
 
 }  // namespace iqk

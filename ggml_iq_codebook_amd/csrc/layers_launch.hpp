@@ -105,7 +105,7 @@ struct Fp4Product {
 };
 int64_t fp4_workspace(int dtype, const void* x, int64_t ldx, int64_t tokens, int64_t rows,
                       int experts, int64_t channels, int64_t depth);
-hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, int cus, hipStream_t stream);
+hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, hipStream_t stream);
 
 // The router: rows of logits.
 struct Logits {
