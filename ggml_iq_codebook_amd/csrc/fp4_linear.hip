@@ -14,6 +14,7 @@
 
 #include "expert_tiles.hpp"
 #include "fp4_common.hpp"
+#include "fp4_sizes.hpp"
 #include "layers_launch.hpp"
 #include "row_codes.hpp"
 
@@ -689,19 +690,17 @@ hipError_t launch_size(int size, const Fp4Product& p, void* workspace, hipStream
     }
     switch (size) {
     case 1016: return launch_few<kDT, 1, 1, 8, kExperts>(p, stream);
-    case 2016: return launch_few<kDT, 2, 1, 8, kExperts>(p, stream);
     case 4016: return launch_few<kDT, 4, 1, 8, kExperts>(p, stream);
     case 8016: return launch_few<kDT, 8, 1, 8, kExperts>(p, stream);
     case 16032: return launch_few<kDT, 16, 2, 8, kExperts>(p, stream);
     // Of fp32 the parts of 32 rows leave LDS for four waves, and those of 64 no room.
     case 32032: return launch_few<kDT, 32, 2, kDT == IQ_DTYPE_F32 ? 4 : 8, kExperts>(p, stream);
     case 64032:
-        if constexpr (kDT == IQ_DTYPE_BF16) return launch_few<kDT, 64, 2, 8, kExperts>(p, stream);
+        if constexpr (kDT == IQ_DTYPE_BF16 && !kExperts)
+            return launch_few<kDT, 64, 2, 8, kExperts>(p, stream);
         break;
     case 64064: return launch_tiles<kDT, 64, 64, 2, 2, 3, 2, kExperts>(p, parts, stream);
-    case 64128: return launch_tiles<kDT, 64, 128, 2, 4, 4, 2, kExperts>(p, parts, stream);
     case 64256: return launch_tiles<kDT, 64, 256, 1, 8, 3, 1, kExperts>(p, parts, stream);
-    case 128128: return launch_tiles<kDT, 128, 128, 4, 2, 3, 2, kExperts>(p, parts, stream);
     case 128256: return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, kExperts>(p, parts, stream);
     default: break;
     }
@@ -710,8 +709,8 @@ hipError_t launch_size(int size, const Fp4Product& p, void* workspace, hipStream
 
 int choose_size(int dtype, int64_t rows, int64_t channels, int64_t depth, int experts)
 {
-    if (rows > 64 && depth <= kNear / 4) return rows < 1024 ? 128128 : 128256;
-    return rows <= 1 ? 1016 : rows <= 2 ? 2016 : rows <= 4 ? 4016 : rows <= 8 ? 8016 : 16016;
+    const int size = fp4_size(dtype, rows, channels, depth, experts);
+    return is_tile(size) && depth > kNear / 4 ? 16016 : size;
 }
 
 template <bool kExperts>

@@ -176,7 +176,8 @@ def test_rows_around_a_result_are_left_as_they_were():
 PRODUCTS = [(1, 1, 32), (1, 16, 128), (1, 70, 1056), (2, 33, 96), (5, 257, 160), (15, 64, 512), (16, 100, 64),
             (17, 48, 2080), (31, 130, 256), (33, 65, 1024), (48, 512, 288), (64, 63, 4128), (65, 129, 96),
             (100, 260, 544), (127, 64, 128), (129, 300, 224), (200, 17, 1024), (256, 256, 256),
-            (257, 513, 352), (300, 1030, 96), (513, 384, 160)]
+            (257, 513, 352), (300, 1030, 96), (513, 384, 160), (33, 2050, 32), (9, 4100, 1696),
+            (1804, 1100, 352), (1577, 300, 1056), (2007, 2050, 288)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
@@ -333,6 +334,9 @@ EXPERT_CASES = [
     (1, 8, 2, 40, 96, 0.0, None), (4, 16, 2, 130, 160, 0.0, None), (16, 5, 3, 64, 512, 0.3, None),
     (33, 3, 1, 70, 288, 0.0, 1), (100, 70, 2, 48, 64, 0.1, None), (200, 4, 2, 260, 352, 0.5, 3),
     (300, 8, 2, 300, 128, 0.0, 0), (37, 512, 2, 16, 32, 0.0, None), (600, 3, 2, 129, 224, 0.05, 2),
+    (21, 64, 2, 130, 288, 0.0, None), (11, 64, 2, 1100, 32, 0.1, None), (674, 16, 2, 2050, 32, 0.0, 5),
+    (82, 16, 2, 130, 32, 0.0, None), (1079, 64, 2, 70, 32, 0.1, None), (19, 3, 2, 2050, 288, 0.0, None),
+    (623, 64, 2, 70, 352, 0.0, 7),
 ]
 
 
