@@ -335,8 +335,10 @@ struct Parts {
 // steps at a time, and becomes bf16 where it is multiplied, four instructions for 8
 // values.
 //
-// The second half of the waves runs half a step behind (ping-pong): on each SIMD one
-// wave multiplies while the other reads its operands.  A step is two barriers long.
+// Of eight waves, two on a SIMD, the second half runs half a step behind (ping-pong): on
+// each SIMD one wave multiplies while the other reads its operands.  A step is two
+// barriers long.  Four waves go together, a step a barrier, and it is other workgroups
+// of the compute unit that fill the gaps.
 template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
           bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel(Fp4Product p,
@@ -345,6 +347,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
 {
     typedef typename Value<kDT>::raw raw;
     constexpr int kWaves = kWT * kWC, kThreads = kWaves * kWave;
+    constexpr bool kPingPong = kWaves == 8;
     constexpr int kFT = kRows / kWT / 16, kFC = kChannels / kWC / 16;
     constexpr int kParts = kSplit<kDT>;
     constexpr int kRowsPerLoad = 4;   // of 256 bytes each
@@ -504,47 +507,74 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     fetch_scales(1);
     fetch_codes(1);
     constexpr int kLeft = (kStages - 2) * kLoads;
-    const bool late = wave >= kWaves / 2;
-    wait_and_meet<kLeft + kCodes>();
-    if (late) asm volatile("s_barrier" ::: "memory");
     // A chunk of the weight is as many steps of each part of the activations.
     constexpr int kSteps = kChunk * kParts, kTurn = kScales / kGroups;
     int buffer = 0;
-    for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+    auto store_weight = [&](int chunk) {
+        store_codes((chunk + 1) % 2);
+        if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
+    };
+    // Step s + kStages - 1 into the buffer of the step before s, and at a chunk's first
+    // step (u) the weight two chunks ahead.
+    auto fetch_ahead = [&](int s, int u, int chunk) {
+        fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
+        buffer = buffer + 1 == kStages ? 0 : buffer + 1;
+        if (u == 0) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
+            fetch_codes(chunk + 2);
+        }
+    };
+    if constexpr (kPingPong) {
+        const bool late = wave >= kWaves / 2;
+        wait_and_meet<kLeft + kCodes>();
+        if (late) asm volatile("s_barrier" ::: "memory");
+        for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int s = s0 + u;
-            if (s >= steps) break;
-            // The chunk before, whose buffer this is, was read before the last barrier.
-            if (u == 0) {
-                store_codes((chunk + 1) % 2);
-                if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
-            }
-            read(buffer, chunk * kChunk + u / kParts, u / kParts);
-            // Into the buffer of the step before, which both halves read before the
-            // last barrier.
-            fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
-            buffer = buffer + 1 == kStages ? 0 : buffer + 1;
-            if (u == 0) {
+            for (int u = 0; u < kSteps; ++u) {
+                const int s = s0 + u;
+                if (s >= steps) break;
+                // The chunk before, whose buffer this is, was read before the last barrier,
+                // as both halves read the step before.
+                if (u == 0) store_weight(chunk);
+                read(buffer, chunk * kChunk + u / kParts, u / kParts);
+                fetch_ahead(s, u, chunk);
+                // The next step has to be there.  The weight's codes were asked for behind
+                // the copies of step s0 + kStages - 1.
+                if (u <= kStages - 2)
+                    wait_and_meet<kLeft + kCodes>();
+                else
+                    wait_and_meet<kLeft>();
                 __builtin_amdgcn_sched_barrier(0);
-                if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
-                fetch_codes(chunk + 2);
+                __builtin_amdgcn_s_setprio(1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                asm volatile("s_barrier" ::: "memory");
             }
-            // The next step has to be there.  The weight's codes were asked for behind the
-            // copies of step s0 + kStages - 1.
-            if (u <= kStages - 2)
-                wait_and_meet<kLeft + kCodes>();
-            else
-                wait_and_meet<kLeft>();
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_setprio(1);
-            multiply();
-            __builtin_amdgcn_s_setprio(0);
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("s_barrier" ::: "memory");
+        }
+        if (!late) asm volatile("s_barrier" ::: "memory");
+    } else {
+        for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int s = s0 + u;
+                if (s >= steps) break;
+                // This step has to be there, and the others are done with the one before.
+                // The codes last asked for are behind the copies of the chunk's step
+                // kStages - 1, or of that step of the chunk before.
+                if (u == 0 ? kSteps < kStages : u < kStages)
+                    wait_and_meet<kLeft + kCodes>();
+                else
+                    wait_and_meet<kLeft>();
+                if (u == 0) store_weight(chunk);
+                const int b = buffer;
+                fetch_ahead(s, u, chunk);
+                read(b, chunk * kChunk + u / kParts, u / kParts);
+                multiply();
+            }
         }
     }
-    if (!late) asm volatile("s_barrier" ::: "memory");
 
     // Results through LDS, as the matrix instructions leave them (4 channels of a row
     // to a lane), and out as whole rows of the wave's channels, 16 bytes a lane.
@@ -677,51 +707,53 @@ hipError_t launch_few(const Fp4Product& p, hipStream_t stream)
     });
 }
 
-// Whether a size, as rows * 1000 + channels, is one of the tile kernel's.
-bool is_tile(int size) { return size % 1000 >= 64; }
-
-template <int kDT, bool kExperts>
-hipError_t launch_size(int size, const Fp4Product& p, void* workspace, hipStream_t stream)
+template <int kDT>
+hipError_t launch_dense(int size, const Fp4Product& p, const Parts& x, hipStream_t stream)
 {
-    Parts parts = {static_cast<const uint16_t*>(p.x), p.ldx, p.depth};
-    if (is_tile(size) && !direct(p.dtype, p.x, p.ldx, p.tokens)) {
-        const hipError_t e = launch_split<kDT>(p, workspace, &parts, stream);
-        if (e != hipSuccess) return e;
-    }
     switch (size) {
-    case 1016: return launch_few<kDT, 1, 1, 8, kExperts>(p, stream);
-    case 4016: return launch_few<kDT, 4, 1, 8, kExperts>(p, stream);
-    case 8016: return launch_few<kDT, 8, 1, 8, kExperts>(p, stream);
-    case 16032: return launch_few<kDT, 16, 2, 8, kExperts>(p, stream);
-    // Of fp32 the parts of 32 rows leave LDS for four waves, and those of 64 no room.
-    case 32032: return launch_few<kDT, 32, 2, kDT == IQ_DTYPE_F32 ? 4 : 8, kExperts>(p, stream);
-    case 64032:
-        if constexpr (kDT == IQ_DTYPE_BF16 && !kExperts)
-            return launch_few<kDT, 64, 2, 8, kExperts>(p, stream);
+    case size_key(1, 16, 8): return launch_few<kDT, 1, 1, 8, false>(p, stream);
+    case size_key(4, 16, 8): return launch_few<kDT, 4, 1, 8, false>(p, stream);
+    case size_key(8, 16, 8): return launch_few<kDT, 8, 1, 8, false>(p, stream);
+    case size_key(16, 16, 8): return launch_few<kDT, 16, 1, 8, false>(p, stream);
+    case size_key(16, 32, 8):
+        // bf16 has always a faster one.
+        if constexpr (kDT != IQ_DTYPE_BF16) return launch_few<kDT, 16, 2, 8, false>(p, stream);
         break;
-    case 64064: return launch_tiles<kDT, 64, 64, 2, 2, 3, 2, kExperts>(p, parts, stream);
-    case 64256: return launch_tiles<kDT, 64, 256, 1, 8, 3, 1, kExperts>(p, parts, stream);
-    case 128256: return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, kExperts>(p, parts, stream);
+    case size_key(32, 32, 8):
+        // The parts of 32 rows of fp32 do not fit LDS.
+        if constexpr (kDT != IQ_DTYPE_F32) return launch_few<kDT, 32, 2, 8, false>(p, stream);
+        break;
+    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, 1, false>(p, x, stream);
+    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, 1, false>(p, x, stream);
+    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, 1, false>(p, x, stream);
+    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, false>(p, x, stream);
     default: break;
     }
-    return launch_few<kDT, 16, 1, 8, kExperts>(p, stream);
+    return launch_few<kDT, 16, 1, 4, false>(p, stream);
 }
 
+template <int kDT>
+hipError_t launch_experts(int size, const Fp4Product& p, const Parts& x, hipStream_t stream)
+{
+    switch (size) {
+    case size_key(1, 16, 4): return launch_few<kDT, 1, 1, 4, true>(p, stream);
+    case size_key(4, 16, 4): return launch_few<kDT, 4, 1, 4, true>(p, stream);
+    case size_key(8, 16, 4): return launch_few<kDT, 8, 1, 4, true>(p, stream);
+    case size_key(8, 32, 4): return launch_few<kDT, 8, 2, 4, true>(p, stream);
+    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, 1, true>(p, x, stream);
+    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, 1, true>(p, x, stream);
+    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, 1, true>(p, x, stream);
+    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, true>(p, x, stream);
+    default: return launch_few<kDT, 16, 2, 4, true>(p, stream);
+    }
+}
+
+// 0: the kernel of few rows, whatever its size, where the depth is beyond the reach of
+// the tile kernel's offsets.
 int choose_size(int dtype, int64_t rows, int64_t channels, int64_t depth, int experts)
 {
     const int size = fp4_size(dtype, rows, channels, depth, experts);
-    return is_tile(size) && depth > kNear / 4 ? 16016 : size;
-}
-
-template <bool kExperts>
-hipError_t launch_product(const Fp4Product& p, void* workspace, hipStream_t stream)
-{
-    int size = choose_size(p.dtype, p.rows, p.channels, p.depth, p.experts);
-    // Strides that 32-bit offsets do not reach: the kernel of few rows takes any.
-    if (is_tile(size) && (p.ldw > kNear || p.lds > kNear)) size = 16016;
-    return with_dtype(p.dtype, [&](auto dt) {
-        return launch_size<decltype(dt)::value, kExperts>(size, p, workspace, stream);
-    });
+    return is_tile(size) && depth > kNear / 4 ? 0 : size;
 }
 
 }  // namespace
@@ -737,8 +769,19 @@ int64_t fp4_workspace(int dtype, const void* x, int64_t ldx, int64_t tokens, int
 
 hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, hipStream_t stream)
 {
-    return p.experts ? launch_product<true>(p, workspace, stream)
-                     : launch_product<false>(p, workspace, stream);
+    int size = choose_size(p.dtype, p.rows, p.channels, p.depth, p.experts);
+    // So too where the weight's rows are too far apart.
+    if (is_tile(size) && (p.ldw > kNear || p.lds > kNear)) size = 0;
+    return with_dtype(p.dtype, [&](auto dt) {
+        constexpr int kDT = decltype(dt)::value;
+        Parts x = {static_cast<const uint16_t*>(p.x), p.ldx, p.depth};
+        if (is_tile(size) && !direct(p.dtype, p.x, p.ldx, p.tokens)) {
+            const hipError_t e = launch_split<kDT>(p, workspace, &x, stream);
+            if (e != hipSuccess) return e;
+        }
+        return p.experts ? launch_experts<kDT>(size, p, x, stream)
+                         : launch_dense<kDT>(size, p, x, stream);
+    });
 }
 
 }  // namespace iqk

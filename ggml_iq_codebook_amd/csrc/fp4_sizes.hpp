@@ -1,100 +1,141 @@
-// fp4_sizes.hpp -- how many rows and channels a workgroup of a product with 4-bit
-// weights takes: the size with the least expected time.  Host code only.
+// fp4_sizes.hpp -- how many rows, channels and waves a workgroup of a product with
+// 4-bit weights has: the size with the least expected time.  Host code only.
 //
-// Sizes of 64 channels and more are the tile kernel's (64 x 64, 64 x 256 and 128 x
-// 256), the others those of the kernel for few rows, which has its operands in
-// registers and reads a weight again for each of its row tiles.  The constants are fits
-// to measured times like those of int8_tiles.hpp, made by perf/fp4_sizes.py from
-// profiles/sizes_fp4.json.  Sizes that were tried and are not worth their code: 2 x 16,
-// 64 x 128 and 128 x 128 (under 0.3 % on average, 64 x 128 1.2 % by expert in bf16).
-// The times hold for 256 compute units, a whole card: the choice also sizes the
-// workspace, which has to be the same wherever it is asked.
+// Sizes of 64 channels and more are the tile kernel's, the others those of the kernel
+// of few rows, which reads a weight again for each of its row tiles and is taken up to
+// 12 of them.  Dense products of few rows have a workgroup to a compute unit, whose
+// eight waves share the depth; those by expert have many, and smaller ones hide each
+// other's start (16 tokens, 2 of 16 experts of 1536 x 4096: 20.7 us with eight waves of
+// 4 x 16, 15.1 with four of 4 x 32).  The constants are fits to measured times, made by
+// perf/fp4_sizes.py from profiles/sizes_fp4.json.  The times hold for 256 compute units,
+// a whole card: the choice also sizes the workspace, which has to be the same wherever
+// it is asked.
 #pragma once
 
-#include "int8_tiles.hpp"
+#include <cmath>
+#include <cstdint>
+
 #include "iq_codec.h"
 
 namespace iqk {
 
-// To 420 products of bf16 activations, 1 to 4096 rows: 0.3 % longer than the fastest
-// on average, 16 % at worst.
-constexpr TileTime kDenseBf16[] = {
-    {1, 16, 3.07, 0.32, 0.22, 0.47, 0.0},
-    {4, 16, 3.14, 0.38, 0.28, 0.34, 0.0},
-    {8, 16, 3.2, 0.44, 0.33, 0.32, 0.03},
-    {16, 16, 3.29, 0.54, 0.42, 0.19, 0.07},
-    {16, 32, 2.31, 2.37, 0.64, 0.2, 0.27},
-    {32, 32, 2.27, 3.14, 0.77, 0.0, 0.6},
-    {64, 32, 2.02, 4.9, 1.45, 0.0, 0.79},
-    {64, 64, 5.13, 0.0, 3.23, 1.69, 0.0},
-    {64, 256, 3.08, 2.99, 7.63, 4.43, 1.17},
-    {128, 256, 3.16, 4.99, 9.1, 5.52, 3.13}};
-// To 320 of fp16 ones: 0.7 %, 25 % at worst.
-constexpr TileTime kDenseF16[] = {
-    {1, 16, 3.36, 0.24, 0.28, 0.52, 0.01},
-    {4, 16, 3.39, 0.33, 0.43, 0.52, 0.0},
-    {8, 16, 3.54, 0.2, 0.63, 0.57, 0.0},
-    {16, 16, 3.87, 0.23, 1.0, 0.6, 0.0},
-    {16, 32, 2.05, 3.06, 1.18, 0.0, 0.43},
-    {32, 32, 2.11, 4.08, 1.99, 0.02, 0.65},
-    {64, 64, 8.07, 0.0, 6.63, 1.67, 0.0},
-    {64, 256, 7.27, 1.87, 14.9, 5.96, 2.49},
-    {128, 256, 10.14, 0.43, 19.78, 11.59, 2.69}};
-// To 320 of fp32 ones: 0.5 %, 46 % at worst.
-constexpr TileTime kDenseF32[] = {
-    {1, 16, 3.53, 0.01, 0.35, 0.63, 0.05},
-    {4, 16, 3.46, 0.37, 0.57, 0.43, 0.0},
-    {8, 16, 3.47, 0.3, 0.84, 0.45, 0.0},
-    {16, 16, 1.86, 2.26, 1.36, 0.42, 0.17},
-    {16, 32, 2.42, 2.31, 1.66, 0.9, 0.25},
-    {32, 32, 2.73, 3.68, 3.09, 0.0, 1.84},
-    {64, 64, 9.09, 0.0, 9.76, 1.98, 0.0},
-    {64, 256, 9.99, 0.0, 19.95, 9.24, 4.96},
-    {128, 256, 12.32, 0.68, 28.93, 15.41, 3.6}};
+// The expected time in microseconds: `once` for the product, for each turn of `slots`
+// workgroups that share a compute unit `start` and, for every 1024 of the depth, `depth`;
+// `start_full` and `depth_full` count with the workgroups that a unit has on average.
+struct Fp4Size {
+    int rows, channels, waves, slots;
+    double once, start, depth, start_full, depth_full;
+};
+
+// To 420 products of bf16 activations, 1 to 4096 rows: 0.8 % longer than the fastest
+// on average, 37 % at worst.
+constexpr Fp4Size kDenseBf16[] = {
+    {1, 16, 8, 2, 2.62, 1.0, 0.16, 0.34, 0.15},
+    {4, 16, 8, 1, 3.12, 0.56, 0.26, 0.11, 0.04},
+    {8, 16, 8, 1, 3.3, 0.39, 0.32, 0.32, 0.05},
+    {16, 16, 4, 4, 3.03, 0.59, 0.56, 0.25, 0.32},
+    {16, 16, 8, 1, 3.35, 0.5, 0.43, 0.22, 0.07},
+    {32, 32, 8, 1, 2.45, 2.95, 0.81, 0.1, 0.55},
+    {32, 64, 4, 5, 3.49, 0.78, 2.41, 0.64, 1.17},
+    {32, 128, 4, 3, 2.39, 2.17, 3.29, 0.56, 2.24},
+    {64, 128, 4, 2, 2.5, 2.62, 4.84, 1.17, 2.84},
+    {128, 256, 8, 1, 3.66, 4.04, 8.85, 5.51, 4.72}};
+// To 320 of fp16 ones: 1.3 %, 143 % at worst.
+constexpr Fp4Size kDenseF16[] = {
+    {1, 16, 8, 1, 3.26, 0.59, 0.29, 0.1, 0.0},
+    {4, 16, 8, 1, 3.36, 0.55, 0.43, 0.2, 0.0},
+    {8, 16, 8, 1, 3.37, 0.56, 0.63, 0.15, 0.0},
+    {16, 16, 4, 4, 2.78, 1.3, 1.29, 0.29, 0.53},
+    {16, 16, 8, 1, 3.77, 0.48, 0.99, 0.29, 0.0},
+    {16, 32, 8, 1, 2.51, 2.62, 1.16, 0.0, 0.43},
+    {32, 32, 8, 1, 1.64, 4.52, 1.99, 0.0, 0.53},
+    {32, 64, 4, 4, 6.89, 0.0, 6.05, 0.84, 1.89},
+    {32, 128, 4, 3, 6.94, 0.0, 7.67, 1.53, 3.04},
+    {64, 128, 4, 2, 7.76, 0.0, 11.78, 3.38, 3.53},
+    {128, 256, 8, 1, 10.6, 0.6, 20.0, 12.41, 3.19}};
+// To 320 of fp32 ones: 0.8 %, 100 % at worst.
+constexpr Fp4Size kDenseF32[] = {
+    {1, 16, 8, 2, 2.64, 0.94, 0.32, 0.45, 0.23},
+    {4, 16, 8, 1, 3.47, 0.43, 0.53, 0.29, 0.04},
+    {8, 16, 8, 2, 2.9, 0.96, 0.69, 0.4, 0.49},
+    {16, 16, 4, 3, 3.55, 0.62, 1.66, 0.25, 0.8},
+    {16, 16, 8, 1, 2.06, 2.31, 1.24, 0.0, 0.42},
+    {16, 32, 8, 1, 2.31, 2.78, 1.49, 0.0, 0.63},
+    {32, 64, 4, 3, 7.15, 0.0, 8.85, 1.46, 1.58},
+    {32, 128, 4, 3, 7.2, 0.0, 10.25, 2.62, 4.14},
+    {64, 128, 4, 2, 6.57, 1.45, 16.21, 5.5, 4.71},
+    {128, 256, 8, 1, 12.11, 1.8, 26.83, 13.8, 9.59}};
 // To 360 products by expert of bf16 activations, 8 to 128 experts, chosen evenly and
-// not: 2.7 %, 45 % at worst.
-constexpr TileTime kExpertBf16[] = {
-    {1, 16, 3.41, 0.0, 0.22, 0.98, 0.04},
-    {4, 16, 3.76, 0.0, 0.19, 1.4, 0.19},
-    {8, 16, 3.68, 0.0, 0.3, 1.43, 0.16},
-    {16, 16, 3.98, 0.0, 0.4, 1.6, 0.15},
-    {16, 32, 3.05, 1.95, 0.72, 1.99, 0.38},
-    {32, 32, 2.46, 4.51, 0.71, 0.58, 0.74},
-    {64, 64, 5.74, 0.0, 2.34, 2.35, 1.18},
-    {64, 256, 2.93, 3.45, 7.4, 4.57, 1.41},
-    {128, 256, 4.22, 4.35, 9.21, 5.15, 2.46}};
-// To 280 of fp16 ones: 3.1 %, 62 % at worst.
-constexpr TileTime kExpertF16[] = {
-    {1, 16, 3.44, 0.0, 0.13, 1.11, 0.15},
-    {4, 16, 3.66, 0.0, 0.44, 1.65, 0.0},
-    {8, 16, 3.47, 0.11, 0.6, 1.58, 0.0},
-    {16, 16, 4.06, 0.0, 0.92, 1.9, 0.0},
-    {16, 32, 3.46, 1.91, 0.68, 2.47, 1.04},
-    {32, 32, 2.9, 5.38, 0.47, 0.19, 2.28},
-    {64, 64, 8.06, 0.0, 5.42, 2.75, 0.66},
-    {64, 256, 5.41, 2.01, 14.69, 6.91, 0.4},
-    {128, 256, 9.66, 2.47, 19.92, 7.04, 2.51}};
-// To 280 of fp32 ones: 3.2 %, 48 % at worst.
-constexpr TileTime kExpertF32[] = {
-    {1, 16, 3.37, 1.1, 0.0, 0.0, 0.35},
-    {4, 16, 3.77, 1.12, 0.32, 0.56, 0.21},
-    {8, 16, 3.61, 1.25, 0.57, 0.35, 0.19},
-    {16, 16, 3.22, 2.49, 0.75, 0.82, 0.83},
-    {16, 32, 2.36, 4.49, 0.55, 0.0, 1.53},
-    {32, 32, 3.77, 5.13, 0.0, 0.0, 4.87},
-    {64, 64, 8.85, 0.0, 7.4, 3.11, 1.52},
-    {64, 256, 8.33, 1.39, 15.9, 5.94, 6.43},
-    {128, 256, 4.13, 9.26, 29.45, 5.74, 2.33}};
+// not: 1.8 %, 57 % at worst.
+constexpr Fp4Size kExpertBf16[] = {
+    {1, 16, 4, 8, 2.43, 2.12, 0.07, 0.17, 0.22},
+    {4, 16, 4, 5, 3.45, 1.22, 0.17, 0.22, 0.33},
+    {8, 16, 4, 4, 3.01, 1.86, 0.17, 0.11, 0.43},
+    {8, 32, 4, 3, 3.19, 2.25, 0.39, 0.28, 0.65},
+    {16, 32, 4, 3, 3.24, 2.67, 0.55, 0.37, 0.74},
+    {32, 64, 4, 5, 3.89, 1.46, 2.61, 0.74, 1.32},
+    {32, 128, 4, 3, 4.39, 1.05, 3.85, 1.22, 2.08},
+    {64, 128, 4, 2, 3.18, 3.03, 5.51, 1.29, 2.86},
+    {128, 256, 8, 1, 2.6, 7.05, 8.45, 3.16, 3.63}};
+// To 280 of fp16 ones: 2.1 %, 62 % at worst.
+constexpr Fp4Size kExpertF16[] = {
+    {1, 16, 4, 6, 2.31, 2.52, 0.31, 0.13, 0.19},
+    {4, 16, 4, 4, 2.81, 2.2, 0.55, 0.24, 0.31},
+    {8, 16, 4, 4, 2.96, 2.13, 0.84, 0.21, 0.41},
+    {8, 32, 4, 3, 2.95, 3.1, 0.84, 0.22, 0.65},
+    {16, 32, 4, 3, 4.44, 1.93, 1.23, 0.68, 0.86},
+    {32, 64, 4, 5, 6.46, 1.06, 5.62, 1.01, 2.03},
+    {32, 128, 4, 4, 7.56, 0.02, 6.69, 1.87, 3.66},
+    {64, 128, 4, 2, 6.6, 1.08, 12.54, 3.24, 2.66},
+    {128, 256, 8, 1, 6.62, 3.9, 19.92, 6.82, 3.58}};
+// To 280 of fp32 ones: 2.0 %, 51 % at worst.
+constexpr Fp4Size kExpertF32[] = {
+    {1, 16, 4, 5, 2.64, 1.73, 0.38, 0.25, 0.23},
+    {4, 16, 4, 5, 3.57, 0.97, 0.67, 0.57, 0.42},
+    {8, 16, 4, 4, 3.57, 0.97, 1.07, 0.52, 0.5},
+    {8, 32, 4, 2, 3.81, 1.19, 1.38, 1.18, 0.63},
+    {16, 32, 4, 2, 3.32, 3.44, 1.32, 0.38, 1.15},
+    {32, 64, 4, 5, 6.11, 1.55, 7.68, 1.1, 3.06},
+    {32, 128, 4, 3, 7.52, 0.0, 10.44, 2.46, 3.86},
+    {64, 128, 4, 2, 7.56, 0.55, 17.47, 4.08, 3.53},
+    {128, 256, 8, 1, 8.53, 3.01, 27.83, 12.5, 5.22}};
+
+// A size as one number.
+constexpr int size_key(int rows, int channels, int waves)
+{
+    return (rows * 1000 + channels) * 100 + waves;
+}
+// Whether it is the tile kernel's.
+constexpr bool is_tile(int key) { return key / 100 % 1000 >= 64; }
 
 template <int kN>
 inline int fastest_size(int64_t rows, int64_t channels, int64_t depth, int experts,
-                        const TileTime (&sizes)[kN])
+                        const Fp4Size (&sizes)[kN])
 {
-    const TileTime& t = sizes[fastest_tile(rows, channels, depth, experts, 256, sizes)];
-    return t.rows * 1000 + t.channels;
+    int best = 0;
+    double least = 0.0;
+    for (const Fp4Size& s : sizes) {
+        double tiles = (double)((rows + s.rows - 1) / s.rows), each = (double)rows;
+        if (experts) {
+            // As if every row chose its expert evenly: the last tile of an expert that
+            // has rows is half full.
+            each /= experts;
+            const double used = experts * (1.0 - std::exp(-each));
+            tiles = std::fmax(used, (double)rows / s.rows + 0.5 * used);
+        }
+        if (s.channels < 64 && each > 12.0 * s.rows) continue;
+        const double average = tiles * (double)((channels + s.channels - 1) / s.channels) / 256.0;
+        const double k = depth / 1024.0;
+        const double time = s.once + std::ceil(average / s.slots) * (s.start + s.depth * k) +
+                            average * (s.start_full + s.depth_full * k);
+        if (!best || time < least) {
+            least = time;
+            best = size_key(s.rows, s.channels, s.waves);
+        }
+    }
+    return best;
 }
 
-// As rows * 1000 + channels.
 inline int fp4_size(int dtype, int64_t rows, int64_t channels, int64_t depth, int experts)
 {
     if (experts)

@@ -177,7 +177,8 @@ PRODUCTS = [(1, 1, 32), (1, 16, 128), (1, 70, 1056), (2, 33, 96), (5, 257, 160),
             (17, 48, 2080), (31, 130, 256), (33, 65, 1024), (48, 512, 288), (64, 63, 4128), (65, 129, 96),
             (100, 260, 544), (127, 64, 128), (129, 300, 224), (200, 17, 1024), (256, 256, 256),
             (257, 513, 352), (300, 1030, 96), (513, 384, 160), (33, 2050, 32), (9, 4100, 1696),
-            (1804, 1100, 352), (1577, 300, 1056), (2007, 2050, 288)]
+            (1804, 1100, 352), (1577, 300, 1056), (161, 70, 1280), (1455, 2050, 224), (33, 2050, 1056),
+            (1229, 5000, 256)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
@@ -336,7 +337,9 @@ EXPERT_CASES = [
     (300, 8, 2, 300, 128, 0.0, 0), (37, 512, 2, 16, 32, 0.0, None), (600, 3, 2, 129, 224, 0.05, 2),
     (21, 64, 2, 130, 288, 0.0, None), (11, 64, 2, 1100, 32, 0.1, None), (674, 16, 2, 2050, 32, 0.0, 5),
     (82, 16, 2, 130, 32, 0.0, None), (1079, 64, 2, 70, 32, 0.1, None), (19, 3, 2, 2050, 288, 0.0, None),
-    (623, 64, 2, 70, 352, 0.0, 7),
+    (623, 64, 2, 70, 352, 0.0, 7), (38, 64, 2, 1100, 288, 0.0, None), (945, 8, 2, 2050, 32, 0.1, None),
+    (98, 2, 2, 70, 416, 0.0, None), (471, 2, 2, 1100, 32, 0.0, None), (47, 3, 1, 2050, 2176, 0.0, None),
+    (555, 3, 2, 5000, 64, 0.0, 1),
 ]
 
 

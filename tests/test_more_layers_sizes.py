@@ -16,7 +16,6 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, os.path.join(ROOT, "perf"))
 
 import fp4_sizes  # noqa: E402
-import tiles  # noqa: E402
 
 CSRC = os.path.join(ROOT, "ggml_iq_codebook_amd", "csrc")
 TABLES = {"bf16 dense": "kDenseBf16", "f16 dense": "kDenseF16", "f32 dense": "kDenseF32",
@@ -34,7 +33,7 @@ extern "C" int size(int dtype, int64_t rows, int64_t channels, int64_t depth, in
 def table(name):
     """The entries of a table in the header, and its comment."""
     text = open(os.path.join(CSRC, "fp4_sizes.hpp")).read()
-    before, body = text.split("constexpr TileTime %s[] = {" % name)
+    before, body = text.split("constexpr Fp4Size %s[] = {" % name)
     comment = " ".join(l[3:] for l in before.splitlines()[-3:] if l.startswith("// "))
     rows = re.findall(r"\{([^{}]+)\}", body.split("};")[0] + "}")
     return [tuple(float(v) for v in r.split(",")) for r in rows], comment
@@ -54,28 +53,35 @@ def rule(tmp_path_factory):
     return f
 
 
+def key(size):
+    rows, channels, waves = fp4_sizes.numbers(size)
+    return (rows * 1000 + channels) * 100 + waves
+
+
 @pytest.mark.parametrize("name", TABLES)
 def test_tables_are_the_fit(name):
     data = fp4_sizes.measured()[name]
-    constants = tiles.fit(data)
-    want = [(*tiles.size(t), *constants[t]) for t in data["tiles"]]
+    fitted = fp4_sizes.fit(data)
+    want = [(*fp4_sizes.numbers(s), slots, *constants) for s, (slots, constants) in fitted.items()]
     got, comment = table(TABLES[name])
     assert got == [tuple(float(v) for v in w) for w in want]
-    ratios = tiles.excess(data, constants, data["tiles"])
-    assert "To %d " % len(data["products"]) in comment
-    assert "%.1f %%" % (100 * tiles.mean(ratios) - 100) in comment
+    ratios = fp4_sizes.excess(data, fitted)
+    assert len(ratios) == len(data["products"])
+    assert "To %d " % len(ratios) in comment
+    assert "%.1f %%" % (100 * fp4_sizes.mean(ratios) - 100) in comment
     assert "%.0f %% at worst" % (100 * max(ratios) - 100) in comment
 
 
 @pytest.mark.parametrize("name", TABLES)
 def test_the_rule_is_the_fits(rule, name):
     data = fp4_sizes.measured()[name]
-    constants = tiles.fit(data)
+    fitted = fp4_sizes.fit(data)
     dtype = DTYPES[name.split()[0]]
     for *product, _ in data["products"]:
-        t = tiles.choice(constants, data["tiles"], *product)
-        tall, wide = tiles.size(t)
-        assert rule(dtype, *product) == tall * 1000 + wide, product
+        assert rule(dtype, *product) == key(fp4_sizes.choice(fitted, data["sizes"], *product)), product
+    # beyond what was measured there is a size too
+    for product in ((1, 1, 32), (2 ** 31 - 1, 1, 32), (1, 2 ** 30 - 1, 32), (2 ** 31 - 1, 2 ** 30 - 1, 2 ** 30)):
+        assert rule(dtype, *product, 512 if "expert" in name else 0) in [key(s) for s in data["sizes"]]
 
 
 def shapes(name):
@@ -89,8 +95,7 @@ def shapes(name):
 
 def test_gpu_tests_take_every_size(rule):
     for kind, dtype in ((k, d) for k in ("dense", "by expert") for d in DTYPES):
-        sizes = {(lambda s: s[0] * 1000 + s[1])(tiles.size(t))
-                 for t in fp4_sizes.measured()["%s %s" % (dtype, kind)]["tiles"]}
+        sizes = {key(s) for s in fp4_sizes.measured()["%s %s" % (dtype, kind)]["sizes"]}
         if kind == "dense":
             taken = {rule(DTYPES[dtype], t, n, k, 0) for t, n, k in shapes("PRODUCTS")}
         else:
