@@ -103,7 +103,7 @@ iq_status_t iq_expert_balance(iq_dtype_t dtype, const void* logits, int64_t ldl,
     const int bytes = value_bytes(dtype);
     if (!bytes || !aligned(logits, bytes) || (choice_bytes != 4 && choice_bytes != 8) ||
         !aligned(choice, choice_bytes) || !aligned(loss, 4) || !aligned(counts, 4) ||
-        !aligned(live, 4) || !aligned(workspace, 4) || workspace_bytes < need ||
+        !aligned(live, 4) || !aligned(workspace, 8) || workspace_bytes < need ||
         (status && !aligned(status, 4)))
         return IQ_ERR_ARG;
     if (overlaps({array(loss, 1, 4), array(counts, experts, 4), array(live, 1, 4),

@@ -23,7 +23,37 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kNone = -__builtin_inff();
 
-// op over the kL lanes of a row, the same result in all of them.
+// v of the lanes of the other 16 of 32 (kDistance 16) or the other 32 (32): both, of this
+// half and of the other, in an order that is the same for all lanes.
+template <int kDistance>
+__device__ __forceinline__ void both_halves(uint32_t v, uint32_t (&half)[2])
+{
+    typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+    const v2u swapped = __builtin_bit_cast(
+        v2u, kDistance == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                             : __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    half[0] = swapped[0];
+    half[1] = swapped[1];
+}
+template <int kDistance, class T, class Op>
+__device__ __forceinline__ T halves(T v, Op&& op)
+{
+    static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
+    uint32_t u[sizeof(T) / 4], low[2], high[2] = {};
+    __builtin_memcpy(u, &v, sizeof(T));
+    both_halves<kDistance>(u[0], low);
+    if constexpr (sizeof(T) == 8) both_halves<kDistance>(u[1], high);
+    T half[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        u[0] = low[i];
+        if constexpr (sizeof(T) == 8) u[1] = high[i];
+        __builtin_memcpy(&half[i], u, sizeof(T));
+    }
+    return op(half[0], half[1]);
+}
+
+// op over the kL lanes of a row (64: a wave), the same result in all of them.
 template <int kL, class T, class Op>
 __device__ __forceinline__ T across(T v, Op&& op)
 {
@@ -31,7 +61,8 @@ __device__ __forceinline__ T across(T v, Op&& op)
     if constexpr (kL > 2) v = op(v, quad_xchg<kQuadXor2>(v));
     if constexpr (kL > 4) v = op(v, quad_xchg<0x141>(v));     // lane 7 - i of 8
     if constexpr (kL > 8) v = op(v, quad_xchg<0x140>(v));     // lane 15 - i of 16
-    if constexpr (kL > 16) v = op(v, __shfl_xor(v, 16));
+    if constexpr (kL > 16) v = halves<16>(v, op);
+    if constexpr (kL > 32) v = halves<32>(v, op);
     return v;
 }
 
@@ -46,6 +77,17 @@ __device__ __forceinline__ T sum_across(T v)
     return across<kL>(v, [](T a, T b) { return a + b; });
 }
 
+// The sum over the rows of a wave, kL lanes each, of what their lanes of one place have.
+template <int kL, class T>
+__device__ __forceinline__ T sum_rows(T v)
+{
+    const auto add = [](T a, T b) { return a + b; };
+    if constexpr (kL <= 4) v = v + quad_xchg<0x124>(v);       // the lane 4 before, of 16
+    if constexpr (kL <= 8) v = v + quad_xchg<0x128>(v);       // the lane 8 before, of 16
+    if constexpr (kL <= 16) v = halves<16>(v, add);
+    return halves<32>(v, add);
+}
+
 // A row of logits: lane `lane` of kL has kC vectors, experts at(c) .. + kN - 1.
 template <int kDT, int kL, int kC>
 struct LogitRow {
@@ -57,16 +99,28 @@ struct LogitRow {
     bool bad;
     __device__ __forceinline__ static int at(int lane, int c) { return (c * kL + lane) * kN; }
     __device__ __forceinline__ static int expert(int lane, int i) { return at(lane, i / kN) + i % kN; }
+    // The row as it is stored, to be asked for ahead.
+    struct Stored {
+        Row<kDT> r[kC];
+        __device__ __forceinline__ void load(const Logits& l, int64_t row, int lane)
+        {
+            const raw* from = static_cast<const raw*>(l.p) + row * l.ld;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) r[c].load(from, at(lane, c), l.experts);
+        }
+    };
     __device__ __forceinline__ void load(const Logits& l, int64_t row, int lane)
     {
-        const raw* from = static_cast<const raw*>(l.p) + row * l.ld;
-        Row<kDT> r[kC];
-#pragma unroll
-        for (int c = 0; c < kC; ++c) r[c].load(from, at(lane, c), l.experts);
+        Stored stored;
+        stored.load(l, row, lane);
+        take(l, stored, lane);
+    }
+    __device__ __forceinline__ void take(const Logits& l, const Stored& stored, int lane)
+    {
         int wrong = 0;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            v[i] = r[i / kN][i % kN];
+            v[i] = stored.r[i / kN][i % kN];
             if (expert(lane, i) >= l.experts) v[i] = kNone;
             wrong |= !(v[i] < __builtin_inff());
         }
@@ -207,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void expert_gate_backward_kernel(
 // The balance loss
 // ---------------------------------------------------------------------------
 
-constexpr int kSumThreads = 512, kSumWaves = kSumThreads / kWave;
+constexpr int kSumThreads = 1024, kSumWaves = kSumThreads / kWave;
 
 // The loss from the sums of the probabilities and the counts in LDS; all threads,
 // each with its part of the live tokens.
@@ -223,8 +277,7 @@ __device__ __forceinline__ void finish(const double* probability, const int* cou
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-#pragma unroll
-        for (int d = kWave / 2; d; d >>= 1) sum[i] += __shfl_xor(sum[i], d);
+        sum[i] = sum_across<kWave>(sum[i]);
         if (threadIdx.x % kWave == 0) parts[i][threadIdx.x / kWave] = sum[i];
     }
     __syncthreads();
@@ -259,6 +312,8 @@ __global__ __launch_bounds__(kSumThreads) void expert_balance_kernel(
     const int64_t r1 = l.tokens * (blockIdx.x + 1) / gridDim.x;
     for (int e = threadIdx.x; e < kMost; e += kSumThreads) count[e] = 0;
     if (threadIdx.x == 0) live = 0;
+    typename R::Stored next;
+    if (r0 + threadIdx.x / kL < r1) next.load(l, r0 + threadIdx.x / kL, lane);
     __syncthreads();
 
     for (int64_t i = r0 * top_k + threadIdx.x; i < r1 * top_k; i += kSumThreads) {
@@ -275,7 +330,8 @@ __global__ __launch_bounds__(kSumThreads) void expert_balance_kernel(
     int mine = 0, n = 0;
     for (int64_t row = r0 + threadIdx.x / kL; row < r1; row += kRows) {
         R r;
-        r.load(l, row, lane);
+        r.take(l, next, lane);
+        if (row + kRows < r1) next.load(l, row + kRows, lane);
         if (r.bad && lane == 0) report_generic(status, IQ_ERR_NONFINITE);
         if (r.live()) {
             float e[R::kV];
@@ -295,9 +351,7 @@ __global__ __launch_bounds__(kSumThreads) void expert_balance_kernel(
     if (lane == 0 && mine) atomicAdd(&live, mine);
 #pragma unroll
     for (int i = 0; i < R::kV; ++i) {
-        long_sum[i] += (double)sum[i];
-#pragma unroll
-        for (int d = kL; d < kWave; d <<= 1) long_sum[i] += __shfl_xor(long_sum[i], d);
+        long_sum[i] = sum_rows<kL>(long_sum[i] + (double)sum[i]);
         if (threadIdx.x % kWave < kL)
             wave_sums[threadIdx.x / kWave][R::expert(lane, i)] = long_sum[i];
     }
@@ -321,38 +375,86 @@ __global__ __launch_bounds__(kSumThreads) void expert_balance_kernel(
     }
 }
 
-__global__ __launch_bounds__(kSumThreads) void expert_balance_finish_kernel(
-    int experts, int parts, const float* __restrict__ sums, const int32_t* __restrict__ part_counts,
-    const int32_t* __restrict__ part_live, float* loss, int32_t* counts, int32_t* tokens)
+// The parts' sums added up.  A workgroup has 16 experts, so that what the parts left,
+// which comes from beyond the L2, comes to many compute units; with more than one
+// workgroup their shares of the loss are added by the kernel below.
+constexpr int kFinishExperts = 16, kFinishThreads = 256;
+constexpr int kFinishSlices = kFinishThreads / kFinishExperts;
+
+struct Share {
+    double dot, total;                // sum of probability * count, and of counts
+};
+
+__device__ __forceinline__ void write_loss(Share s, int live, int experts, float* loss, int32_t* tokens)
 {
-    __shared__ double probability[IQ_MAX_EXPERTS];
-    __shared__ int count[IQ_MAX_EXPERTS];
-    __shared__ double slice_sums[kSumThreads];
-    __shared__ int slice_counts[kSumThreads];
-    // Threads beside each other have experts beside each other; slices of threads
-    // share the parts.
-    const int wide = experts <= 64 ? 64 : (experts <= 128 ? 128 : (experts <= 256 ? 256 : 512));
-    const int slices = kSumThreads / wide, slice = threadIdx.x / wide, e = threadIdx.x % wide;
+    *tokens = live;
+    *loss = s.dot > 0.0 ? (float)(experts * s.dot / (s.total * live)) : 0.0f;
+}
+
+// The live tokens of all parts, in every lane of a wave.
+__device__ __forceinline__ int live_tokens(const int32_t* part_live, int parts)
+{
+    int live = 0;
+    for (int i = threadIdx.x % kWave; i < parts; i += kWave) live += part_live[i];
+    return sum_across<kWave>(live);
+}
+
+__global__ __launch_bounds__(kFinishThreads) void expert_balance_finish_kernel(
+    int experts, int parts, const float* __restrict__ sums, const int32_t* __restrict__ part_counts,
+    const int32_t* __restrict__ part_live, float* loss, int32_t* counts, int32_t* tokens,
+    Share* shares)
+{
+    __shared__ double slice_sums[kFinishSlices][kFinishExperts];
+    __shared__ int slice_counts[kFinishSlices][kFinishExperts];
+    const int slice = threadIdx.x / kFinishExperts, at = threadIdx.x % kFinishExperts;
+    const int e = blockIdx.x * kFinishExperts + at;
     double sum = 0.0;
-    int number = 0, live = 0;
-    if (e < experts)
-        for (int i = slice; i < parts; i += slices) {
+    int number = 0;
+    if (e < experts) {
+#pragma unroll 8
+        for (int i = slice; i < parts; i += kFinishSlices) {
             sum += (double)sums[(int64_t)i * experts + e];
             number += part_counts[(int64_t)i * experts + e];
         }
-    for (int i = threadIdx.x; i < parts; i += kSumThreads) live += part_live[i];
-    slice_sums[threadIdx.x] = sum;
-    slice_counts[threadIdx.x] = number;
-    __syncthreads();
-    if (threadIdx.x < experts) {
-        for (int i = 1; i < slices; ++i) {
-            sum += slice_sums[i * wide + e];
-            number += slice_counts[i * wide + e];
-        }
-        probability[e] = sum;
-        count[e] = number;
     }
-    finish(probability, count, live, experts, loss, counts, tokens);
+    slice_sums[slice][at] = sum;
+    slice_counts[slice][at] = number;
+    __syncthreads();
+    if (threadIdx.x >= kWave) return;
+    Share share = {0.0, 0.0};
+    if (threadIdx.x < kFinishExperts && e < experts) {
+        sum = 0.0;
+        number = 0;
+#pragma unroll
+        for (int i = 0; i < kFinishSlices; ++i) {
+            sum += slice_sums[i][at];
+            number += slice_counts[i][at];
+        }
+        counts[e] = number;
+        share = {sum * (double)number, (double)number};
+    }
+    share.dot = sum_across<kFinishExperts>(share.dot);
+    share.total = sum_across<kFinishExperts>(share.total);
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) shares[blockIdx.x] = share;
+        return;
+    }
+    const int live = live_tokens(part_live, parts);
+    if (threadIdx.x == 0) write_loss(share, live, experts, loss, tokens);
+}
+
+__global__ __launch_bounds__(kWave) void expert_balance_loss_kernel(
+    int experts, int parts, const Share* __restrict__ shares, const int32_t* __restrict__ part_live,
+    float* loss, int32_t* tokens)
+{
+    static_assert(IQ_MAX_EXPERTS / kFinishExperts <= kWave, "a lane for every workgroup");
+    const int workgroups = (experts + kFinishExperts - 1) / kFinishExperts;
+    Share share = {0.0, 0.0};
+    if ((int)threadIdx.x < workgroups) share = shares[threadIdx.x];
+    share.dot = sum_across<kWave>(share.dot);
+    share.total = sum_across<kWave>(share.total);
+    const int live = live_tokens(part_live, parts);
+    if (threadIdx.x == 0) write_loss(share, live, experts, loss, tokens);
 }
 
 // p (counts_e - sum_j counts_j p_j) E g / (C N) for each row.
@@ -410,14 +512,6 @@ __global__ __launch_bounds__(kThreads) void expert_balance_backward_kernel(
     }
 }
 
-// How many workgroups share the loss's sums.  The rule sizes the workspace too, so
-// it asks nothing of the device.
-int balance_parts(int64_t tokens, int experts)
-{
-    const int64_t rows = experts <= 64 ? 64 : 32;
-    return (int)std::min<int64_t>(256, std::max<int64_t>(1, tokens / rows / 4));
-}
-
 // body(lanes, vectors) for a number of experts: the lanes of a row and the vectors
 // of 16 bytes that each of them has.
 template <int kDT, class Body>
@@ -429,6 +523,21 @@ hipError_t with_row(int experts, Body&& body)
     if (experts <= 128) return body(Int<16>(), Int<8 / kN>());
     if (experts <= 256) return body(Int<16>(), Int<16 / kN>());
     return body(Int<32>(), Int<16 / kN>());
+}
+
+// The lanes of a row, as above.
+int row_lanes(int experts)
+{
+    return experts <= 32 ? 4 : (experts <= 64 ? 8 : (experts <= 256 ? 16 : 32));
+}
+
+// How many workgroups share the loss's sums: alone what they take at once, otherwise at
+// most one for every compute unit of a whole card.  (The rule sizes the workspace too, so
+// it asks nothing of the device.)
+int balance_parts(int64_t tokens, int experts)
+{
+    const int64_t rows = kSumThreads / row_lanes(experts);
+    return (int)std::min<int64_t>(256, std::max<int64_t>(1, (tokens + rows - 1) / rows));
 }
 
 template <class Body>
@@ -474,10 +583,13 @@ hipError_t launch_expert_gate_backward(const Logits& l, const float* weights_gra
     });
 }
 
+constexpr int64_t kShareBytes = IQ_MAX_EXPERTS / kFinishExperts * (int64_t)sizeof(Share);
+
 int64_t balance_workspace(int64_t tokens, int experts)
 {
     const int64_t parts = balance_parts(tokens, experts);
-    return parts > 1 ? parts * (2 * (int64_t)experts + 1) * 4 : 0;
+    // The shares of the loss first, then the parts' sums, counts and live tokens.
+    return parts > 1 ? kShareBytes + parts * (2 * (int64_t)experts + 1) * 4 : 0;
 }
 
 hipError_t launch_expert_balance(const Logits& l, const void* choice, int choice_bytes, int top_k,
@@ -485,7 +597,8 @@ hipError_t launch_expert_balance(const Logits& l, const void* choice, int choice
                                  int32_t* status, hipStream_t stream)
 {
     const int parts = balance_parts(l.tokens, l.experts);
-    float* sums = static_cast<float*>(workspace);
+    Share* shares = static_cast<Share*>(workspace);
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + kShareBytes);
     int32_t* part_counts = reinterpret_cast<int32_t*>(sums + (int64_t)parts * l.experts);
     int32_t* part_live = part_counts + (int64_t)parts * l.experts;
     const hipError_t e = with_logits(l, [&](auto dt, auto lanes, auto vectors) {
@@ -502,8 +615,13 @@ hipError_t launch_expert_balance(const Logits& l, const void* choice, int choice
         return hipGetLastError();
     });
     if (e != hipSuccess || parts == 1) return e;
-    hipLaunchKernelGGL(expert_balance_finish_kernel, dim3(1), dim3(kSumThreads), 0, stream,
-                       l.experts, parts, sums, part_counts, part_live, loss, counts, live);
+    const int wgs = (l.experts + kFinishExperts - 1) / kFinishExperts;
+    hipLaunchKernelGGL(expert_balance_finish_kernel, dim3(wgs), dim3(kFinishThreads), 0, stream,
+                       l.experts, parts, sums, part_counts, part_live, loss, counts, live, shares);
+    const hipError_t f = hipGetLastError();
+    if (f != hipSuccess || wgs == 1) return f;
+    hipLaunchKernelGGL(expert_balance_loss_kernel, dim3(1), dim3(kWave), 0, stream, l.experts, parts,
+                       shares, part_live, loss, live);
     return hipGetLastError();
 }
 

@@ -44,7 +44,7 @@ iq_status_t iq_expert_gate_backward(iq_dtype_t dtype, const float* weights_grad,
  * choice is what iq_expert_sort takes ([tokens][top_k], choice_bytes 4 or 8, -1 for
  * dropped); others out of range are reported as IQ_ERR_INDEX and not counted, a
  * token with a NaN or +inf as IQ_ERR_NONFINITE.  `workspace`:
- * iq_expert_balance_workspace(tokens, experts) bytes, 4-byte aligned (NULL where
+ * iq_expert_balance_workspace(tokens, experts) bytes, 8-byte aligned (NULL where
  * that is 0); it need not be cleared. */
 int64_t iq_expert_balance_workspace(int64_t tokens, int32_t experts);
 iq_status_t iq_expert_balance(iq_dtype_t dtype, const void* logits, int64_t ldl, int64_t tokens,

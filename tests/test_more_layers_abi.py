@@ -140,7 +140,7 @@ def test_a_workspace_that_is_missing_or_short(lib):
     big = dict(t=100000, e=64, ld=64, l=P(1 << 32), c=P(2 << 32))
     assert balance(lib, **big) == NULL
     assert balance(lib, wk=P(3 << 32), wb=need - 1, **big) == ARG
-    assert balance(lib, wk=P((3 << 32) + 2), wb=need, **big) == ARG
+    assert balance(lib, wk=P((3 << 32) + 4), wb=need, **big) == ARG
 
 
 # --- overlaps ---------------------------------------------------------------
