@@ -29,4 +29,20 @@ __device__ __forceinline__ v8bf values_of(uint32_t codes, float scale)
     return __builtin_bit_cast(v8bf, v);
 }
 
+// The same as fp16: exact for scale bytes kLowF16 .. kHighF16, where half of the lowest
+// power is 2^-24 and 6 times the highest below 2^16.  Values of other bytes may not be
+// representable.
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+constexpr uint32_t kLowF16 = 104, kHighF16 = 140;
+
+__device__ __forceinline__ v8h half_values_of(uint32_t codes, float scale)
+{
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    const v2h v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2),
+                      __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3)};
+    return __builtin_bit_cast(v8h, v);
+}
+
 }  // namespace iqk

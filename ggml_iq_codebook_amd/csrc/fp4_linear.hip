@@ -3,14 +3,17 @@
 //   y[t][n] = sum_k x[t][k] * value(w[n][k]).
 //
 // The weight's values are exact in bf16, so the matrix cores take them as they
-// are.  bf16 activations are an operand as they come; fp16 ones are split into
-// two bf16 parts and fp32 ones into three (v = hi + mid + lo exactly), each
-// multiplied in turn, so every product is exact and only the fp32 sums and the
-// one rounding of the result differ from the formula.  (The parts of fp32 values
-// below 2^-110 reach below bf16's smallest number, 2^-133, and are cut there.)
+// are.  bf16 activations are an operand as they come; fp32 ones are split into
+// three bf16 parts (v = hi + mid + lo exactly), each multiplied in turn.  fp16
+// activations are an operand of fp16 products while the weight's scales are in
+// fp16's range, 2^-23 .. 2^13, and split into two bf16 parts where one is not.
+// Every product is exact that way, and only the fp32 sums and the one rounding of
+// the result differ from the formula.  (The parts of fp32 values below 2^-110
+// reach below bf16's smallest number, 2^-133, and are cut there.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "expert_tiles.hpp"
 #include "fp4_common.hpp"
@@ -40,6 +43,16 @@ __device__ __forceinline__ v4u load16(const uint8_t* from)
     return v;
 }
 
+__device__ __forceinline__ v4f mfma16(v8h a, v8h b, v4f c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Parts in which activations wait in LDS: fp32 is split on the way there, the others
+// come as they are.
+template <int kDT>
+constexpr int kStaged = kDT == IQ_DTYPE_F32 ? 3 : 1;
+
 // bf16 parts that a type is split into.
 template <int kDT>
 constexpr int kSplit = kDT == IQ_DTYPE_BF16 ? 1 : (kDT == IQ_DTYPE_F16 ? 2 : 3);
@@ -65,7 +78,15 @@ __device__ __forceinline__ void split_values(const typename Value<kDT>::raw (&r)
                 left = left - __uint_as_float(u[k][i] & 0xffff0000u);
             }
         }
-        if (top >= 0x7f800000u) {
+        if constexpr (kDT == IQ_DTYPE_F16) {
+            // Without a branch, which costs a kernel registers.
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = u[0][i] & 0x7fffffffu;
+                u[0][i] = bits > 0x7f800000u ? 0x7fc00000u : u[0][i];
+                u[1][i] = bits >= 0x7f800000u ? 0u : u[1][i];
+            }
+        } else if (top >= 0x7f800000u) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (finite_f32(Value<kDT>::load(r[i]))) continue;
@@ -87,17 +108,34 @@ __device__ __forceinline__ void split_values(const typename Value<kDT>::raw (&r)
     }
 }
 
-// The scale bytes g0 .. g0 + 15 of a row that ends before, 0 beyond its end.
+// Whether the values of a lane's groups are exact in fp16: scales within its range, or
+// zeros only.
+template <int kN>
+__device__ __forceinline__ bool exact_in_f16(const v4u (&word)[kN], const uint32_t (&byte)[kN])
+{
+    bool exact = true;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const v4u w = word[i];
+        exact &= byte[i] - kLowF16 <= kHighF16 - kLowF16 ||
+                 ((w.x | w.y | w.z | w.w) & 0x77777777u) == 0u;
+    }
+    return exact;
+}
+
+// The scale bytes g0 .. g0 + 15 of a row that ends before, that of 1 beyond its end.
 __device__ __forceinline__ v4u last_scales(const uint8_t* row, int g0, int groups)
 {
     unsigned __int128 v = 0;
-    if (g0 >= groups) return v4u{0u, 0u, 0u, 0u};
+    constexpr uint32_t kOnes = 0x7f7f7f7fu;
+    if (g0 >= groups) return v4u{kOnes, kOnes, kOnes, kOnes};
     if (groups >= 16) {
         v = __builtin_bit_cast(unsigned __int128, load16(row + groups - 16)) >> 8 * (g0 + 16 - groups);
     } else {
 #pragma unroll 1
         for (int i = 0; i < groups - g0; ++i) v |= (unsigned __int128)row[g0 + i] << 8 * i;
     }
+    v |= __builtin_bit_cast(unsigned __int128, v4u{kOnes, kOnes, kOnes, kOnes}) << 8 * (groups - g0);
     return __builtin_bit_cast(v4u, v);
 }
 
@@ -139,7 +177,7 @@ template <int kDT, int kTok, int kFC, int kWaves, bool kExperts>
 __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, int channel_tiles)
 {
     typedef typename Value<kDT>::raw raw;
-    constexpr int kN = kSplit<kDT>, kChannels = 16 * kFC, kThreads = kWaves * kWave;
+    constexpr int kN = kStaged<kDT>, kChannels = 16 * kFC, kThreads = kWaves * kWave;
     constexpr int kFT = (kTok + 15) / 16;
     constexpr int kBlock = 4;
     // Steps whose activations are staged at once, 8 values each to a lane kX times.
@@ -209,7 +247,10 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
             v8bf part[kN];
             raw r[8];
             __builtin_memcpy(r, held[i].r, sizeof(r));
-            split_values<kDT>(r, part);
+            if constexpr (kN > 1)
+                split_values<kDT>(r, part);
+            else
+                part[0] = __builtin_bit_cast(v8bf, r);
 #pragma unroll
             for (int q = 0; q < kN; ++q)
                 *reinterpret_cast<v8bf*>(&shared.x[wave][q][unit / kUnits][unit % kUnits * 8]) = part[q];
@@ -217,23 +258,53 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
     };
     v4f acc[kFC][kFT] = {};
     auto multiply = [&](int in_sub, const v4u (&word)[kFC], const v4u (&scales_of)[kFC], int j) {
+        uint32_t byte[kFC];
+#pragma unroll
+        for (int i = 0; i < kFC; ++i) byte[i] = scales_of[i][j] >> 8 * quarter & 0xffu;
+        auto operand = [&](int f, int q, int k) {
+            return *reinterpret_cast<const v8bf*>(
+                &shared.x[wave][q][(16 * f + lane % 16) % kTok][in_sub * kPiece + 32 * quarter + 8 * k]);
+        };
+        if constexpr (kDT == IQ_DTYPE_F16) {
+            if (__all(exact_in_f16(word, byte))) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v8h b[kFT];
+#pragma unroll
+                    for (int f = 0; f < kFT; ++f) b[f] = __builtin_bit_cast(v8h, operand(f, 0, k));
+#pragma unroll
+                    for (int i = 0; i < kFC; ++i) {
+                        const v8h a = half_values_of(word[i][k], group_scale(byte[i]));
+#pragma unroll
+                        for (int f = 0; f < kFT; ++f) acc[i][f] = mfma16(a, b[f], acc[i][f]);
+                    }
+                }
+                return;
+            }
+        }
+        constexpr int kS = kSplit<kDT>;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            v8bf b[kFT][kN];
+            v8bf b[kFT][kS];
 #pragma unroll
-            for (int f = 0; f < kFT; ++f)
+            for (int f = 0; f < kFT; ++f) {
+                if constexpr (kS > kN) {
+                    raw r[8];
+                    const v8bf v = operand(f, 0, k);
+                    __builtin_memcpy(r, &v, sizeof(r));
+                    split_values<kDT>(r, b[f]);
+                } else {
 #pragma unroll
-                for (int q = 0; q < kN; ++q)
-                    b[f][q] = *reinterpret_cast<const v8bf*>(
-                        &shared.x[wave][q][(16 * f + lane % 16) % kTok]
-                                 [in_sub * kPiece + 32 * quarter + 8 * k]);
+                    for (int q = 0; q < kS; ++q) b[f][q] = operand(f, q, k);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kFC; ++i) {
-                const v8bf a = values_of(word[i][k], group_scale(scales_of[i][j] >> 8 * quarter & 0xffu));
+                const v8bf a = values_of(word[i][k], group_scale(byte[i]));
 #pragma unroll
                 for (int f = 0; f < kFT; ++f)
 #pragma unroll
-                    for (int q = kN - 1; q >= 0; --q) acc[i][f] = mfma16(a, b[f][q], acc[i][f]);
+                    for (int q = kS - 1; q >= 0; --q) acc[i][f] = mfma16(a, b[f][q], acc[i][f]);
             }
         }
     };
@@ -318,9 +389,9 @@ __device__ __forceinline__ void wait_and_meet()
 
 __device__ const uint16_t kZeros[8] __attribute__((aligned(16))) = {};
 
-// x as bf16 parts, those of each piece one after another, in rows of ldx values
-// that start on 16 bytes and have `width` of them: bf16 activations as they are where
-// they do (one part), others as split_kernel lays them out.
+// x in rows of ldx values that start on 16 bytes and have `width` of them: 16-bit
+// activations as they are where they do, others as split_kernel lays them out, the
+// three bf16 parts of each piece of fp32 one after another.
 struct Parts {
     const uint16_t* x;
     int64_t ldx;
@@ -349,7 +420,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     constexpr int kWaves = kWT * kWC, kThreads = kWaves * kWave;
     constexpr bool kPingPong = kWaves == 8;
     constexpr int kFT = kRows / kWT / 16, kFC = kChannels / kWC / 16;
-    constexpr int kParts = kSplit<kDT>;
+    constexpr int kParts = kStaged<kDT>;
     constexpr int kRowsPerLoad = 4;   // of 256 bytes each
     constexpr int kLoads = kRows / kRowsPerLoad / kWaves;
     // Groups of a chunk, 16 bytes of codes each, and a thread's part of them.
@@ -432,7 +503,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
 #pragma unroll
         for (int i = 0; i < kCodes; ++i) staged.codes[b][i * kThreads + threadIdx.x] = codes[i];
     };
-    // Groups beyond the last, whose activations are zeros, have the smallest scale.
+    // Groups beyond the last, whose activations are zeros, have the scale 1.
     v4u scales = {};
     auto fetch_scales = [&](int chunk) {
         if (threadIdx.x >= kScaleThreads) return;
@@ -473,19 +544,16 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
                     &staged.x[b][r * kPiece + ((4 * quarter + k) ^ (lane % 16)) * 8]);
             }
     };
-    auto multiply = [&]() {
-        auto operand = [&](int f) {
-            return values_of(word[f % kFC][f / kFC], group_scale(byte[f % kFC]));
-        };
-        v8bf a = operand(0), next = a;
+    // The products of one kind of operand, the next one's conversions among those of one.
+    auto multiply_as = [&](auto&& operand, auto&& activations) {
+        auto a = operand(0), next = a;
 #pragma unroll
         for (int f = 0; f < 4 * kFC; ++f) {
             if (f + 1 < 4 * kFC) next = operand(f + 1);
 #pragma unroll
             for (int j = 0; j < kFT; ++j)
-                acc[f % kFC][j] = mfma16(a, x[f / kFC][j], acc[f % kFC][j]);
+                acc[f % kFC][j] = mfma16(a, activations(f / kFC, j), acc[f % kFC][j]);
             a = next;
-            // The next operand's conversions among these products.
             constexpr int kEach = kFT >= 4 ? 1 : 4 / kFT;
 #pragma unroll
             for (int i = 0; i < 4 / kEach; ++i) {
@@ -494,85 +562,128 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
             }
         }
     };
+    // fp16 activations are multiplied as fp16 as long as the weight is exact in it.
+    bool exact = true;
+    auto multiply = [&](auto in_f16) {
+        auto weight = [&](int f) { return values_of(word[f % kFC][f / kFC], group_scale(byte[f % kFC])); };
+        if constexpr (kDT != IQ_DTYPE_F16) {
+            multiply_as(weight, [&](int k, int j) { return x[k][j]; });
+        } else if constexpr (in_f16) {
+            exact &= exact_in_f16(word, byte);
+            multiply_as([&](int f) { return half_values_of(word[f % kFC][f / kFC],
+                                                           group_scale(byte[f % kFC])); },
+                        [&](int k, int j) { return __builtin_bit_cast(v8h, x[k][j]); });
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < kFT; ++j) {
+                    raw r[8];
+                    v8bf part[kSplit<kDT>];
+                    __builtin_memcpy(r, &x[k][j], sizeof(r));
+                    split_values<kDT>(r, part);
+#pragma unroll
+                    for (int q = kSplit<kDT> - 1; q >= 0; --q)
+#pragma unroll
+                        for (int i = 0; i < kFC; ++i)
+                            acc[i][j] = mfma16(weight(k * kFC + i), part[q], acc[i][j]);
+                    __builtin_amdgcn_sched_barrier(0);  // one at a time, for want of registers
+                }
+        }
+    };
 
     const int steps = (groups + 3) / 4 * kParts;
-    fetch_codes(0);
-    fetch_scales(0);
-    __builtin_amdgcn_sched_barrier(0);
+    auto run = [&](auto in_f16) {
+        fetch_codes(0);
+        fetch_scales(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
-    __builtin_amdgcn_sched_barrier(0);
-    store_codes(0);
-    store_scales(0);
-    fetch_scales(1);
-    fetch_codes(1);
-    constexpr int kLeft = (kStages - 2) * kLoads;
-    // A chunk of the weight is as many steps of each part of the activations.
-    constexpr int kSteps = kChunk * kParts, kTurn = kScales / kGroups;
-    int buffer = 0;
-    auto store_weight = [&](int chunk) {
-        store_codes((chunk + 1) % 2);
-        if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
-    };
-    // Step s + kStages - 1 into the buffer of the step before s, and at a chunk's first
-    // step (u) the weight two chunks ahead.
-    auto fetch_ahead = [&](int s, int u, int chunk) {
-        fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
-        buffer = buffer + 1 == kStages ? 0 : buffer + 1;
-        if (u == 0) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
-            fetch_codes(chunk + 2);
-        }
-    };
-    if constexpr (kPingPong) {
-        const bool late = wave >= kWaves / 2;
-        wait_and_meet<kLeft + kCodes>();
-        if (late) asm volatile("s_barrier" ::: "memory");
-        for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+        __builtin_amdgcn_sched_barrier(0);
+        store_codes(0);
+        store_scales(0);
+        fetch_scales(1);
+        fetch_codes(1);
+        constexpr int kLeft = (kStages - 2) * kLoads;
+        // A chunk of the weight is as many steps of each part of the activations.
+        constexpr int kSteps = kChunk * kParts, kTurn = kScales / kGroups;
+        int buffer = 0;
+        auto store_weight = [&](int chunk) {
+            store_codes((chunk + 1) % 2);
+            if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
+        };
+        // Step s + kStages - 1 into the buffer of the step before s, and at a chunk's first
+        // step (u) the weight two chunks ahead.
+        auto fetch_ahead = [&](int s, int u, int chunk) {
+            fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
+            buffer = buffer + 1 == kStages ? 0 : buffer + 1;
+            if (u == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
+                fetch_codes(chunk + 2);
+            }
+        };
+        if constexpr (kPingPong) {
+            const bool late = wave >= kWaves / 2;
+            wait_and_meet<kLeft + kCodes>();
+            if (late) asm volatile("s_barrier" ::: "memory");
+            for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
 #pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                const int s = s0 + u;
-                if (s >= steps) break;
-                // The chunk before, whose buffer this is, was read before the last barrier,
-                // as both halves read the step before.
-                if (u == 0) store_weight(chunk);
-                read(buffer, chunk * kChunk + u / kParts, u / kParts);
-                fetch_ahead(s, u, chunk);
-                // The next step has to be there.  The weight's codes were asked for behind
-                // the copies of step s0 + kStages - 1.
-                if (u <= kStages - 2)
-                    wait_and_meet<kLeft + kCodes>();
-                else
-                    wait_and_meet<kLeft>();
-                __builtin_amdgcn_sched_barrier(0);
-                __builtin_amdgcn_s_setprio(1);
-                multiply();
-                __builtin_amdgcn_s_setprio(0);
-                __builtin_amdgcn_sched_barrier(0);
-                asm volatile("s_barrier" ::: "memory");
+                for (int u = 0; u < kSteps; ++u) {
+                    const int s = s0 + u;
+                    if (s >= steps) break;
+                    // The chunk before, whose buffer this is, was read before the last barrier,
+                    // as both halves read the step before.
+                    if (u == 0) store_weight(chunk);
+                    read(buffer, chunk * kChunk + u / kParts, u / kParts);
+                    fetch_ahead(s, u, chunk);
+                    // The next step has to be there.  The weight's codes were asked for behind
+                    // the copies of step s0 + kStages - 1.
+                    if (u <= kStages - 2)
+                        wait_and_meet<kLeft + kCodes>();
+                    else
+                        wait_and_meet<kLeft>();
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_setprio(1);
+                    multiply(in_f16);
+                    __builtin_amdgcn_s_setprio(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    asm volatile("s_barrier" ::: "memory");
+                }
+            }
+            if (!late) asm volatile("s_barrier" ::: "memory");
+        } else {
+            for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+                    const int s = s0 + u;
+                    if (s >= steps) break;
+                    // This step has to be there, and the others are done with the one before.
+                    // The codes last asked for are behind the copies of the chunk's step
+                    // kStages - 1, or of that step of the chunk before.
+                    if (u == 0 ? kSteps < kStages : u < kStages)
+                        wait_and_meet<kLeft + kCodes>();
+                    else
+                        wait_and_meet<kLeft>();
+                    if (u == 0) store_weight(chunk);
+                    const int b = buffer;
+                    fetch_ahead(s, u, chunk);
+                    read(b, chunk * kChunk + u / kParts, u / kParts);
+                    multiply(in_f16);
+                }
             }
         }
-        if (!late) asm volatile("s_barrier" ::: "memory");
-    } else {
-        for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+    };
+    run(std::bool_constant<kDT == IQ_DTYPE_F16>());
+    if constexpr (kDT == IQ_DTYPE_F16) {
+        // Otherwise all is done again with bf16 parts.
+        wait_and_meet<0>();
+        if (!__syncthreads_and(exact)) {
 #pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                const int s = s0 + u;
-                if (s >= steps) break;
-                // This step has to be there, and the others are done with the one before.
-                // The codes last asked for are behind the copies of the chunk's step
-                // kStages - 1, or of that step of the chunk before.
-                if (u == 0 ? kSteps < kStages : u < kStages)
-                    wait_and_meet<kLeft + kCodes>();
-                else
-                    wait_and_meet<kLeft>();
-                if (u == 0) store_weight(chunk);
-                const int b = buffer;
-                fetch_ahead(s, u, chunk);
-                read(b, chunk * kChunk + u / kParts, u / kParts);
-                multiply();
-            }
+            for (int i = 0; i < kFC; ++i)
+#pragma unroll
+                for (int j = 0; j < kFT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            run(std::false_type());
         }
     }
 
@@ -619,7 +730,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     }
 }
 
-// Activations split into their bf16 parts, padded to whole pieces with zeros: row t,
+// Activations padded to whole pieces with zeros, fp32 split into its parts: row t,
 // piece c, part q from out[t][(c * kN + q) * 128].
 template <int kDT>
 __global__ __launch_bounds__(256) void split_kernel(const void* __restrict__ x, int64_t ldx,
@@ -627,7 +738,7 @@ __global__ __launch_bounds__(256) void split_kernel(const void* __restrict__ x, 
                                                     int per_row, uint16_t* __restrict__ out)
 {
     typedef typename Value<kDT>::raw raw;
-    constexpr int kN = kSplit<kDT>;
+    constexpr int kN = kStaged<kDT>;
     const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;   // 8 values each
     const int64_t row = i / per_row;
     if (row >= tokens) return;
@@ -636,7 +747,10 @@ __global__ __launch_bounds__(256) void split_kernel(const void* __restrict__ x, 
     if (at < depth)
         __builtin_memcpy(r, static_cast<const raw*>(x) + row * ldx + at, sizeof(r));
     v8bf part[kN];
-    split_values<kDT>(r, part);
+    if constexpr (kN > 1)
+        split_values<kDT>(r, part);
+    else
+        part[0] = __builtin_bit_cast(v8bf, r);
     uint16_t* to = out + (row * per_row * 8 + at / kPiece * kPiece) * kN + at % kPiece;
 #pragma unroll
     for (int q = 0; q < kN; ++q) *reinterpret_cast<v8bf*>(to + q * kPiece) = part[q];
@@ -657,11 +771,9 @@ int64_t workgroups(const Fp4Product& p, int rows, int channel_tiles)
 // bytes, 256 of them within the reach of 32-bit offsets.
 bool direct(int dtype, const void* x, int64_t ldx, int64_t tokens)
 {
-    return dtype == IQ_DTYPE_BF16 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+    return dtype != IQ_DTYPE_F32 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
            (ldx % 8 == 0 || tokens == 1) && ldx <= kNear;
 }
-
-int split_parts(int dtype) { return dtype == IQ_DTYPE_BF16 ? 1 : (dtype == IQ_DTYPE_F16 ? 2 : 3); }
 
 template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
           bool kExperts>
@@ -684,7 +796,7 @@ hipError_t launch_split(const Fp4Product& p, void* workspace, Parts* parts, hipS
 {
     const int per_row = (p.depth + kPiece - 1) / kPiece * (kPiece / 8);
     uint16_t* out = static_cast<uint16_t*>(workspace);
-    const int width = per_row * 8 * kSplit<kDT>;
+    const int width = per_row * 8 * kStaged<kDT>;
     *parts = {out, width, width};
     return in_parts((p.tokens * per_row + 255) / 256, 256, [&](int64_t first, dim3 wgs) {
         hipLaunchKernelGGL(split_kernel<kDT>, wgs, dim3(256), 0, stream, p.x, p.ldx, p.tokens,
@@ -716,8 +828,8 @@ hipError_t launch_dense(int size, const Fp4Product& p, const Parts& x, hipStream
     case size_key(8, 16, 8): return launch_few<kDT, 8, 1, 8, false>(p, stream);
     case size_key(16, 16, 8): return launch_few<kDT, 16, 1, 8, false>(p, stream);
     case size_key(16, 32, 8):
-        // bf16 has always a faster one.
-        if constexpr (kDT != IQ_DTYPE_BF16) return launch_few<kDT, 16, 2, 8, false>(p, stream);
+        // The 16-bit types have a faster one always.
+        if constexpr (kDT == IQ_DTYPE_F32) return launch_few<kDT, 16, 2, 8, false>(p, stream);
         break;
     case size_key(32, 32, 8):
         // The parts of 32 rows of fp32 do not fit LDS.
@@ -739,13 +851,17 @@ hipError_t launch_experts(int size, const Fp4Product& p, const Parts& x, hipStre
     case size_key(1, 16, 4): return launch_few<kDT, 1, 1, 4, true>(p, stream);
     case size_key(4, 16, 4): return launch_few<kDT, 4, 1, 4, true>(p, stream);
     case size_key(8, 16, 4): return launch_few<kDT, 8, 1, 4, true>(p, stream);
-    case size_key(8, 32, 4): return launch_few<kDT, 8, 2, 4, true>(p, stream);
+    case size_key(8, 32, 4):
+        // fp16 has a faster one always.
+        if constexpr (kDT != IQ_DTYPE_F16) return launch_few<kDT, 8, 2, 4, true>(p, stream);
+        break;
     case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, 1, true>(p, x, stream);
     case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, 1, true>(p, x, stream);
     case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, 1, true>(p, x, stream);
     case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, true>(p, x, stream);
-    default: return launch_few<kDT, 16, 2, 4, true>(p, stream);
+    default: break;
     }
+    return launch_few<kDT, 16, 2, 4, true>(p, stream);
 }
 
 // 0: the kernel of few rows, whatever its size, where the depth is beyond the reach of
@@ -764,7 +880,8 @@ int64_t fp4_workspace(int dtype, const void* x, int64_t ldx, int64_t tokens, int
     if (!is_tile(choose_size(dtype, rows, channels, depth, experts)) ||
         direct(dtype, x, ldx, tokens))
         return 0;
-    return tokens * ((depth + kPiece - 1) / kPiece * kPiece) * 2 * split_parts(dtype);
+    return tokens * ((depth + kPiece - 1) / kPiece * kPiece) * 2 *
+           (dtype == IQ_DTYPE_F32 ? kStaged<IQ_DTYPE_F32> : 1);
 }
 
 hipError_t launch_fp4_product(const Fp4Product& p, void* workspace, hipStream_t stream)

@@ -30,29 +30,28 @@ struct Fp4Size {
 // To 420 products of bf16 activations, 1 to 4096 rows: 0.8 % longer than the fastest
 // on average, 37 % at worst.
 constexpr Fp4Size kDenseBf16[] = {
-    {1, 16, 8, 2, 2.62, 1.0, 0.16, 0.34, 0.15},
-    {4, 16, 8, 1, 3.12, 0.56, 0.26, 0.11, 0.04},
-    {8, 16, 8, 1, 3.3, 0.39, 0.32, 0.32, 0.05},
-    {16, 16, 4, 4, 3.03, 0.59, 0.56, 0.25, 0.32},
-    {16, 16, 8, 1, 3.35, 0.5, 0.43, 0.22, 0.07},
-    {32, 32, 8, 1, 2.45, 2.95, 0.81, 0.1, 0.55},
+    {1, 16, 8, 2, 2.59, 1.02, 0.16, 0.34, 0.15},
+    {4, 16, 8, 1, 3.1, 0.57, 0.26, 0.1, 0.04},
+    {8, 16, 8, 1, 3.29, 0.4, 0.32, 0.32, 0.05},
+    {16, 16, 4, 4, 3.03, 0.58, 0.56, 0.25, 0.32},
+    {16, 16, 8, 1, 3.35, 0.51, 0.44, 0.22, 0.06},
+    {32, 32, 8, 1, 2.47, 2.94, 0.81, 0.1, 0.55},
     {32, 64, 4, 5, 3.49, 0.78, 2.41, 0.64, 1.17},
     {32, 128, 4, 3, 2.39, 2.17, 3.29, 0.56, 2.24},
     {64, 128, 4, 2, 2.5, 2.62, 4.84, 1.17, 2.84},
     {128, 256, 8, 1, 3.66, 4.04, 8.85, 5.51, 4.72}};
-// To 320 of fp16 ones: 1.3 %, 143 % at worst.
+// To 320 of fp16 ones: 1.1 %, 27 % at worst.
 constexpr Fp4Size kDenseF16[] = {
-    {1, 16, 8, 1, 3.26, 0.59, 0.29, 0.1, 0.0},
-    {4, 16, 8, 1, 3.36, 0.55, 0.43, 0.2, 0.0},
-    {8, 16, 8, 1, 3.37, 0.56, 0.63, 0.15, 0.0},
-    {16, 16, 4, 4, 2.78, 1.3, 1.29, 0.29, 0.53},
-    {16, 16, 8, 1, 3.77, 0.48, 0.99, 0.29, 0.0},
-    {16, 32, 8, 1, 2.51, 2.62, 1.16, 0.0, 0.43},
-    {32, 32, 8, 1, 1.64, 4.52, 1.99, 0.0, 0.53},
-    {32, 64, 4, 4, 6.89, 0.0, 6.05, 0.84, 1.89},
-    {32, 128, 4, 3, 6.94, 0.0, 7.67, 1.53, 3.04},
-    {64, 128, 4, 2, 7.76, 0.0, 11.78, 3.38, 3.53},
-    {128, 256, 8, 1, 10.6, 0.6, 20.0, 12.41, 3.19}};
+    {1, 16, 8, 1, 3.05, 0.67, 0.25, 0.06, 0.0},
+    {4, 16, 8, 1, 3.35, 0.28, 0.32, 0.42, 0.0},
+    {8, 16, 8, 2, 2.73, 1.09, 0.3, 0.32, 0.26},
+    {16, 16, 4, 4, 2.92, 0.83, 0.65, 0.19, 0.34},
+    {16, 16, 8, 2, 2.72, 1.27, 0.4, 0.34, 0.33},
+    {32, 32, 8, 1, 2.0, 3.51, 0.99, 0.0, 0.45},
+    {32, 64, 4, 4, 2.43, 2.44, 3.09, 0.47, 1.32},
+    {32, 128, 4, 3, 2.53, 2.57, 4.46, 0.86, 2.17},
+    {64, 128, 4, 2, 2.84, 2.64, 7.39, 1.84, 2.51},
+    {128, 256, 8, 1, 2.93, 5.5, 9.31, 5.88, 3.23}};
 // To 320 of fp32 ones: 0.8 %, 100 % at worst.
 constexpr Fp4Size kDenseF32[] = {
     {1, 16, 8, 2, 2.64, 0.94, 0.32, 0.45, 0.23},
@@ -66,28 +65,27 @@ constexpr Fp4Size kDenseF32[] = {
     {64, 128, 4, 2, 6.57, 1.45, 16.21, 5.5, 4.71},
     {128, 256, 8, 1, 12.11, 1.8, 26.83, 13.8, 9.59}};
 // To 360 products by expert of bf16 activations, 8 to 128 experts, chosen evenly and
-// not: 1.8 %, 57 % at worst.
+// not: 1.9 %, 57 % at worst.
 constexpr Fp4Size kExpertBf16[] = {
     {1, 16, 4, 8, 2.43, 2.12, 0.07, 0.17, 0.22},
     {4, 16, 4, 5, 3.45, 1.22, 0.17, 0.22, 0.33},
     {8, 16, 4, 4, 3.01, 1.86, 0.17, 0.11, 0.43},
     {8, 32, 4, 3, 3.19, 2.25, 0.39, 0.28, 0.65},
-    {16, 32, 4, 3, 3.24, 2.67, 0.55, 0.37, 0.74},
-    {32, 64, 4, 5, 3.89, 1.46, 2.61, 0.74, 1.32},
-    {32, 128, 4, 3, 4.39, 1.05, 3.85, 1.22, 2.08},
-    {64, 128, 4, 2, 3.18, 3.03, 5.51, 1.29, 2.86},
-    {128, 256, 8, 1, 2.6, 7.05, 8.45, 3.16, 3.63}};
-// To 280 of fp16 ones: 2.1 %, 62 % at worst.
+    {16, 32, 4, 3, 3.27, 2.63, 0.56, 0.39, 0.72},
+    {32, 64, 4, 5, 3.91, 1.45, 2.6, 0.73, 1.33},
+    {32, 128, 4, 3, 4.36, 1.09, 3.83, 1.19, 2.11},
+    {64, 128, 4, 2, 3.1, 3.14, 5.47, 1.23, 2.91},
+    {128, 256, 8, 1, 2.5, 7.13, 8.53, 3.08, 3.61}};
+// To 280 of fp16 ones: 1.6 %, 37 % at worst.
 constexpr Fp4Size kExpertF16[] = {
-    {1, 16, 4, 6, 2.31, 2.52, 0.31, 0.13, 0.19},
-    {4, 16, 4, 4, 2.81, 2.2, 0.55, 0.24, 0.31},
-    {8, 16, 4, 4, 2.96, 2.13, 0.84, 0.21, 0.41},
-    {8, 32, 4, 3, 2.95, 3.1, 0.84, 0.22, 0.65},
-    {16, 32, 4, 3, 4.44, 1.93, 1.23, 0.68, 0.86},
-    {32, 64, 4, 5, 6.46, 1.06, 5.62, 1.01, 2.03},
-    {32, 128, 4, 4, 7.56, 0.02, 6.69, 1.87, 3.66},
-    {64, 128, 4, 2, 6.6, 1.08, 12.54, 3.24, 2.66},
-    {128, 256, 8, 1, 6.62, 3.9, 19.92, 6.82, 3.58}};
+    {1, 16, 4, 5, 3.0, 1.26, 0.33, 0.27, 0.2},
+    {4, 16, 4, 4, 3.37, 0.88, 0.57, 0.45, 0.23},
+    {8, 16, 4, 4, 3.51, 0.72, 0.62, 0.5, 0.29},
+    {16, 32, 4, 2, 3.15, 2.61, 0.78, 0.68, 0.72},
+    {32, 64, 4, 4, 3.78, 1.59, 4.0, 0.77, 1.43},
+    {32, 128, 4, 3, 4.04, 1.87, 4.52, 1.05, 2.31},
+    {64, 128, 4, 2, 2.53, 4.37, 6.32, 1.07, 2.85},
+    {128, 256, 8, 1, 4.19, 5.33, 9.12, 6.39, 2.29}};
 // To 280 of fp32 ones: 2.0 %, 51 % at worst.
 constexpr Fp4Size kExpertF32[] = {
     {1, 16, 4, 5, 2.64, 1.73, 0.38, 0.25, 0.23},

@@ -178,7 +178,7 @@ PRODUCTS = [(1, 1, 32), (1, 16, 128), (1, 70, 1056), (2, 33, 96), (5, 257, 160),
             (100, 260, 544), (127, 64, 128), (129, 300, 224), (200, 17, 1024), (256, 256, 256),
             (257, 513, 352), (300, 1030, 96), (513, 384, 160), (33, 2050, 32), (9, 4100, 1696),
             (1804, 1100, 352), (1577, 300, 1056), (161, 70, 1280), (1455, 2050, 224), (33, 2050, 1056),
-            (1229, 5000, 256)]
+            (1229, 5000, 256), (1, 70, 1280), (9, 2050, 1056)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
@@ -243,6 +243,29 @@ def test_scales_of_every_size(dtype, tokens):
     x = x.to(dtype).to(DEV)
     want = torch.from_numpy(np.ldexp(to64(x)[:, 37, None], bytes_.numpy() - 127)).float().to(dtype)
     assert torch.equal(iq.fp4_linear(x, w, s.to(DEV)).cpu(), want)
+
+
+@pytest.mark.parametrize("outside", [None, 103, 141, 255])
+@pytest.mark.parametrize("tokens", [1, 5, 30, 100, 700])
+def test_weights_at_the_ends_of_fp16(tokens, outside):
+    """Scales 104 .. 140 with every code are exact in fp16, and a single channel that has
+    another one changes none of the others.  Products by 1/2, 1 and 2 are exact in fp32, the
+    results those rounded once."""
+    depth, n = 160, 37 * 16
+    code = torch.zeros((n, depth), dtype=torch.uint8)
+    code[:, 101] = torch.arange(n) % 16
+    s = torch.full((n, depth // 32), 120, dtype=torch.uint8)
+    s[:, 3] = 104 + torch.arange(n) // 16
+    if outside is not None:
+        code[200, 101], s[200, 3] = 5, outside
+    w = (code[:, 0::2] | (code[:, 1::2] << 4)).to(DEV)
+    x = torch.zeros((tokens, depth))
+    x[:, 101] = torch.tensor([(1.0, 2.0, 0.5)[t % 3] for t in range(tokens)])
+    x = x.half().to(DEV)
+    want = torch.from_numpy(to64(x) @ ref.values(w.cpu().numpy(), s.numpy()).T).float().half()
+    got = iq.fp4_linear(x, w, s.to(DEV)).cpu()
+    assert torch.equal(torch.nan_to_num(got, 1.0), torch.nan_to_num(want, 1.0))
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(got).any() == (outside == 255)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
@@ -339,7 +362,7 @@ EXPERT_CASES = [
     (82, 16, 2, 130, 32, 0.0, None), (1079, 64, 2, 70, 32, 0.1, None), (19, 3, 2, 2050, 288, 0.0, None),
     (623, 64, 2, 70, 352, 0.0, 7), (38, 64, 2, 1100, 288, 0.0, None), (945, 8, 2, 2050, 32, 0.1, None),
     (98, 2, 2, 70, 416, 0.0, None), (471, 2, 2, 1100, 32, 0.0, None), (47, 3, 1, 2050, 2176, 0.0, None),
-    (555, 3, 2, 5000, 64, 0.0, 1),
+    (555, 3, 2, 5000, 64, 0.0, 1), (468, 2, 2, 4100, 160, 0.0, None),
 ]
 
 
@@ -366,6 +389,20 @@ def test_expert_linear(dtype, tokens, experts, top_k, channels, depth, dropped, 
     y, size = expert_reference(to64(x), v, o, f, top_k)
     within(iq.fp4_expert_linear(x, w, s, offsets, order, top_k=top_k), y,
            ref.product_bound(y, size, depth, dtype))
+
+
+@pytest.mark.parametrize("tokens,channels", [(3, 40), (40, 130), (700, 300), (500, 4100)])
+def test_scales_beyond_fp16(tokens, channels):
+    """Of three experts one has scales that fp16 has no room for."""
+    order, _, offsets = routing(tokens, 3, 2, 11)
+    x = normal((tokens, 352), 4, torch.float16)
+    w = random_codes((3, channels, 352), 2)
+    s = random_scale((3, channels, 11), 5, 118, 124)
+    s[1] = random_scale((channels, 11), 6, 90, 124)
+    y, size = expert_reference(to64(x), ref.values(w.cpu().numpy(), s.cpu().numpy()),
+                               order.cpu().numpy(), offsets.cpu().numpy(), 2)
+    within(iq.fp4_expert_linear(x, w, s, offsets, order, top_k=2), y,
+           ref.product_bound(y, size, 352, torch.float16))
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
