@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
     const int first = (int)((int64_t)steps * wave / kWaves);
     const int last = (int)((int64_t)steps * (wave + 1) / kWaves);
 
-    // Beyond the last group, whose activations are zeros: its codes, with scale 0.
+    // Beyond the last group, whose activations are zeros: its codes, with scale 1.
     const uint8_t *w[kFC], *scale[kFC];
 #pragma unroll
     for (int i = 0; i < kFC; ++i) {
@@ -449,11 +449,14 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wt = wave % kWT, wc = wave / kWT;
 
-    // Staged rows in pieces of 16 bytes, piece c in slot c ^ (row % 16): 16 lanes that
-    // read one piece of consecutive rows meet different banks.  Rows beyond the last
-    // repeat it: their results are not stored.
+    // Staged rows in pieces of 16 bytes, piece k of a lane's group q in slot
+    // (4 k + q) ^ (row % 16).  A read of 16 bytes a lane takes 16 lanes at a time, four
+    // neighbours each of different rows and quarters of the wave: with q in the low bits
+    // they meet different banks (with 4 q + k two and two meet, 39 % more LDS cycles:
+    // 4096^3 120 us, now 117).  Rows beyond the last repeat it: their results are not stored.
     auto column = [&](int i) {
-        return ((lane % 16) ^ ((wave * kLoads + i) * kRowsPerLoad + lane / 16) % 16) * 8;
+        const int c = (lane % 16) ^ ((wave * kLoads + i) * kRowsPerLoad + lane / 16) % 16;
+        return (c % 4 * 4 + c / 4) * 8;
     };
     // Dense rows by 32-bit offsets into a buffer that begins at the tile's first row,
     // where an offset beyond its end reads zeros; gathered rows by addresses.
@@ -541,7 +544,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
             for (int j = 0; j < kFT; ++j) {
                 const int r = (wt * kFT + j) * 16 + lane % 16;
                 x[k][j] = *reinterpret_cast<const v8bf*>(
-                    &staged.x[b][r * kPiece + ((4 * quarter + k) ^ (lane % 16)) * 8]);
+                    &staged.x[b][r * kPiece + ((4 * k + quarter) ^ (lane % 16)) * 8]);
             }
     };
     // The products of one kind of operand, the next one's conversions among those of one.
