@@ -9,6 +9,14 @@
 // or a sum of kL values by lane exchanges (no LDS, no barrier).  A logit of -inf
 // is an expert that cannot be chosen, a row of them a token that does not count.
 // A row with a NaN or +inf is reported and treated as such a row.
+//
+// The gate takes k turns of a maximum over the row and the lowest index that has it:
+// bound by latency for few tokens (4 x 64 fp32, 8 chosen: 3.3 us), by instruction issue
+// for many (131072 x 64: 18 us, its bytes 8).  Its gradient and the loss's are a pass
+// over the logits (16384 x 64: 5.8 us; 65536 x 256: 23 us, 5.8 TB/s with what the
+// last level of caches holds).  The loss's forward pass keeps a column's sum in the lanes
+// that have it and asks for the next row while it works on one (65536 x 256: 20.4 us,
+// 3.3 TB/s, bound by its exponentials and sums).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -172,7 +172,10 @@ __device__ __forceinline__ void store_zeros(const Fp4Product& p, const Tile& t)
 // the depth in blocks of 4 steps.  A block of the weight is asked for while the one
 // before is multiplied.  The activations, few of them, are split into their parts once
 // by the lanes together, and every lane takes its operand from there: as operands
-// straight from memory, 16 / kTok times as many would be loaded and split.
+// straight from memory, 16 / kTok times as many would be loaded and split (one token
+// through 4096 x 4096: bf16 5.4 us that way and 3.9 as it is, fp16 10.7 and 4.2, fp32
+// 11.5 and 4.7).  Bound by latency, then by HBM: the weight's 9 MB in 4.7 us, waited for
+// singly; 16 tokens, 2 of 16 experts of 1536 x 4096 47 MB in 16 us.
 template <int kDT, int kTok, int kFC, int kWaves, bool kExperts>
 __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, int channel_tiles)
 {
@@ -410,6 +413,13 @@ struct Parts {
 // each SIMD one wave multiplies while the other reads its operands.  A step is two
 // barriers long.  Four waves go together, a step a barrier, and it is other workgroups
 // of the compute unit that fill the gaps.
+//
+// 128 x 256 at 4096^3 in bf16: 117 us, 1170 TFLOP/s, the matrix cores 52 % busy; a library
+// product of the unpacked weight 97 to 104.  On the way there: the weight straight to
+// registers each step 260 us (a load that touches 16 rows takes 75 cycles to issue), through
+// LDS in steps of 64 of the depth 147, of 128 128, copies by a buffer's 32-bit offsets
+// 124.  Smaller tiles fill the card where there are few: 1021 x 2049 x 1568 in
+// bf16 64 x 64 with four waves 17.4 us, with two halves in turn 24.
 template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
           bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel(Fp4Product p,

@@ -245,6 +245,46 @@ def test_scales_of_every_size(dtype, tokens):
     assert torch.equal(iq.fp4_linear(x, w, s.to(DEV)).cpu(), want)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("tokens,channels,depth", [(3, 40, 160), (300, 130, 352)])
+def test_offsets_beyond_32_bits(dtype, tokens, channels, depth):
+    """Rows so far apart that the last ones begin beyond 2^32 bytes, of one operand at a time."""
+    def apart(t):
+        ld = 2 ** 32 // ((len(t) - 1) * t.element_size()) + 1027
+        far = torch.empty((len(t), ld), dtype=t.dtype, device=DEV)[:, :t.shape[1]]
+        return far.copy_(t)
+
+    x = integers((tokens, depth), 1).to(dtype).to(DEV)
+    w, s = random_codes((channels, depth), 2), random_scale((channels, depth // 32), 3, 126, 128)
+    want = iq.fp4_linear(x, w, s)
+    assert torch.equal(iq.fp4_linear(apart(x), w, s), want)
+    assert torch.equal(iq.fp4_linear(x, apart(w), s), want)
+    assert torch.equal(iq.fp4_linear(x, w, apart(s)), want)
+    out = apart(torch.zeros((tokens, channels), dtype=dtype, device=DEV))
+    assert torch.equal(iq.fp4_linear(x, w, s, out=out), want)
+    order, _, offsets = routing(tokens, 3, 2, 11)
+    w, s = random_codes((3, channels, depth), 2), random_scale((3, channels, depth // 32), 3, 126, 128)
+    want = iq.fp4_expert_linear(x, w, s, offsets, order, top_k=2)
+    assert torch.equal(iq.fp4_expert_linear(apart(x), w, s, offsets, order, top_k=2), want)
+    far = [apart(t.view(3, -1)).unflatten(1, t.shape[1:]) for t in (w, s)]
+    assert torch.equal(iq.fp4_expert_linear(x, *far, offsets, order, top_k=2), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_groups_beyond_32_bits(dtype):
+    x = normal((3, 96), 7, dtype)
+    want = iq.quantize_groups(x)
+    ld = 2 ** 31 // x.element_size() + 5
+    far = torch.empty((3, ld), dtype=dtype, device=DEV)[:, :96]
+    far.copy_(x)
+    got = iq.quantize_groups(far)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    codes, scale = (torch.empty((3, 2 ** 31 + 5), dtype=torch.uint8, device=DEV)[:, :t.shape[1]].copy_(t)
+                    for t in want)
+    assert torch.equal(iq.dequantize_groups(codes, scale, dtype=dtype),
+                       iq.dequantize_groups(*want, dtype=dtype))
+
+
 @pytest.mark.parametrize("outside", [None, 103, 141, 255])
 @pytest.mark.parametrize("tokens", [1, 5, 30, 100, 700])
 def test_weights_at_the_ends_of_fp16(tokens, outside):
