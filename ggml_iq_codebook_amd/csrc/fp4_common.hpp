@@ -29,6 +29,16 @@ __device__ __forceinline__ v8bf values_of(uint32_t codes, float scale)
     return __builtin_bit_cast(v8bf, v);
 }
 
+// Codes whose values are infinite as that of 0: 4 and 6 times 2^126 (bits 2 and 1 of the
+// code), from 2 times 2^127 on (bit 2).
+constexpr uint32_t kInfinite = 253;
+
+__device__ __forceinline__ uint32_t finite_codes(uint32_t codes, uint32_t byte)
+{
+    const uint32_t also = byte == kInfinite ? codes >> 1 : (byte > kInfinite ? ~0u : 0u);
+    return codes & ~((codes >> 2 & also & 0x11111111u) * 15u);
+}
+
 // The same as fp16: exact for scale bytes kLowF16 .. kHighF16, where half of the lowest
 // power is 2^-24 and 6 times the highest below 2^16.  Values of other bytes may not be
 // representable.

@@ -8,8 +8,9 @@
 // activations are an operand of fp16 products while the weight's scales are in
 // fp16's range, 2^-23 .. 2^13, and split into two bf16 parts where one is not.
 // Every product is exact that way, and only the fp32 sums and the one rounding of
-// the result differ from the formula.  (The parts of fp32 values below 2^-110
-// reach below bf16's smallest number, 2^-133, and are cut there.)
+// the result differ from the formula.  (The parts of fp32 values below 2^-110 reach
+// below bf16's smallest number, 2^-133, and are cut there.)  Where a scale reaches
+// beyond fp32, what was summed up in several parts is summed up again with care.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -139,6 +140,70 @@ __device__ __forceinline__ v4u last_scales(const uint8_t* row, int g0, int group
     return __builtin_bit_cast(v4u, v);
 }
 
+// A tile whose rows, the same for all lanes, are kept in scalar registers: the sums below need
+// them late, and a few vector registers more would cost some kernels a workgroup of the compute
+// unit.  (There are below 2^31 rows.)
+__device__ __forceinline__ Tile rows_in_scalars(Tile t)
+{
+    t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
+    t.row_end = __builtin_amdgcn_readfirstlane((int)t.row_end);
+    return t;
+}
+
+// The lanes of the wave whose groups may have infinite values.  (A lane mask is kept in scalar
+// registers.)
+template <int kN>
+__device__ __forceinline__ uint64_t may_be_infinite(const uint32_t (&byte)[kN])
+{
+    uint32_t top = byte[0];
+#pragma unroll
+    for (int i = 1; i < kN; ++i) top = max(top, byte[i]);
+    return __ballot(top >= kInfinite);
+}
+
+// Sums over the depths begin .. end - 1 of a weight with infinite values, for 16 kFC
+// channels from `channel` on and kFT rows of activations for each of 16 lanes.  An infinite
+// value meets the first part of an activation only, which is 0 where the activation is: the
+// others are 0 where the first is all, and 0 times infinity is NaN.  Nothing is asked for
+// ahead, and with the sums done before a product takes 2 to 4 times as long (2048 x 4096 x
+// 4096 of fp32 activations 616 us, 151 where the weight is finite).
+template <int kDT, int kFC, int kFT>
+__device__ __forceinline__ void sum_with_infinities(const Fp4Product& p, int expert, int channel,
+                                                    const typename Value<kDT>::raw* const (&from)[kFT],
+                                                    int begin, int end, v4f (&acc)[kFC][kFT])
+{
+    constexpr int kS = kSplit<kDT>;
+    const int lane = threadIdx.x % kWave, quarter = lane / 16;
+#pragma unroll
+    for (int i = 0; i < kFC; ++i)
+#pragma unroll
+        for (int j = 0; j < kFT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int at = begin; at < end; at += kGroup) {
+        v8bf a[kFC], rest[kFC];
+#pragma unroll
+        for (int i = 0; i < kFC; ++i) {
+            const int64_t n = min(channel + 16 * i + lane % 16, p.channels - 1);
+            const uint32_t byte = p.scale[expert * p.s_stride + n * p.lds + at / kGroup];
+            uint32_t word;
+            __builtin_memcpy(&word, p.w + expert * p.w_stride + n * p.ldw + at / 2 + 4 * quarter, 4);
+            a[i] = values_of(word, group_scale(byte));
+            rest[i] = values_of(finite_codes(word, byte), group_scale(byte));
+        }
+#pragma unroll
+        for (int j = 0; j < kFT; ++j) {
+            typename Value<kDT>::raw r[8];
+            v8bf part[kS];
+            __builtin_memcpy(r, from[j] + at + 8 * quarter, sizeof(r));
+            split_values<kDT>(r, part);
+#pragma unroll
+            for (int q = kS - 1; q >= 0; --q)
+#pragma unroll
+                for (int i = 0; i < kFC; ++i) acc[i][j] = mfma16(q ? rest[i] : a[i], part[q], acc[i][j]);
+        }
+    }
+}
+
 // 4 consecutive channels of one row of y, in its type.
 template <int kDT>
 __device__ __forceinline__ void store_channels(const Fp4Product& p, int64_t row, int channel, v4f f)
@@ -192,7 +257,8 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
         float sums[kWaves][kTok][kChannels];
     };
     __shared__ __align__(16) Shared shared;
-    const Tile t = kExperts ? expert_tile<kTok>(p, channel_tiles) : dense_tile<kTok>(p, channel_tiles);
+    const Tile t = kExperts ? rows_in_scalars(expert_tile<kTok>(p, channel_tiles))
+                            : dense_tile<kTok>(p, channel_tiles);
     if (t.expert == -2) return;
     if (t.expert == -1) {
         store_zeros<kDT, kTok, kChannels, kThreads>(p, t);
@@ -260,10 +326,12 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
         }
     };
     v4f acc[kFC][kFT] = {};
+    uint64_t infinite = 0u;
     auto multiply = [&](int in_sub, const v4u (&word)[kFC], const v4u (&scales_of)[kFC], int j) {
         uint32_t byte[kFC];
 #pragma unroll
         for (int i = 0; i < kFC; ++i) byte[i] = scales_of[i][j] >> 8 * quarter & 0xffu;
+        if constexpr (kSplit<kDT> > 1) infinite |= may_be_infinite(byte);
         auto operand = [&](int f, int q, int k) {
             return *reinterpret_cast<const v8bf*>(
                 &shared.x[wave][q][(16 * f + lane % 16) % kTok][in_sub * kPiece + 32 * quarter + 8 * k]);
@@ -331,6 +399,16 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
         }
     }
 
+    if (kSplit<kDT> > 1 && __builtin_expect(infinite != 0u, 0)) {
+        const raw* rows[kFT];
+#pragma unroll
+        for (int f = 0; f < kFT; ++f) {
+            const int64_t row = min(t.row0 + (16 * f + lane % 16) % kTok, t.row_end - 1);
+            rows[f] = static_cast<const raw*>(p.x) + (kExperts ? token_of(p, row) : row) * p.ldx;
+        }
+        sum_with_infinities<kDT>(p, t.expert, channel0, rows, first * kPiece,
+                                 min(last * kPiece, p.depth), acc);
+    }
     __syncthreads();
     if (lane % 16 < kTok) {
 #pragma unroll
@@ -448,7 +526,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     };
     __shared__ __align__(1024) Staged staged;
 
-    const Tile t = kExperts ? expert_tile<kRows>(p, channel_tiles)
+    const Tile t = kExperts ? rows_in_scalars(expert_tile<kRows>(p, channel_tiles))
                             : dense_tile<kRows>(p, channel_tiles);
     if (t.expert == -2) return;
     if (t.expert == -1) {
@@ -577,7 +655,10 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     };
     // fp16 activations are multiplied as fp16 as long as the weight is exact in it.
     bool exact = true;
-    auto multiply = [&](auto in_f16) {
+    uint64_t infinite = 0u;
+    auto multiply = [&](auto in_f16, int of_part) {
+        if constexpr (kSplit<kDT> > 1 && !in_f16)
+            if (of_part == 0) infinite |= may_be_infinite(byte);
         auto weight = [&](int f) { return values_of(word[f % kFC][f / kFC], group_scale(byte[f % kFC])); };
         if constexpr (kDT != IQ_DTYPE_F16) {
             multiply_as(weight, [&](int k, int j) { return x[k][j]; });
@@ -658,7 +739,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
                         wait_and_meet<kLeft>();
                     __builtin_amdgcn_sched_barrier(0);
                     __builtin_amdgcn_s_setprio(1);
-                    multiply(in_f16);
+                    multiply(in_f16, u % kParts);
                     __builtin_amdgcn_s_setprio(0);
                     __builtin_amdgcn_sched_barrier(0);
                     asm volatile("s_barrier" ::: "memory");
@@ -682,7 +763,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
                     const int b = buffer;
                     fetch_ahead(s, u, chunk);
                     read(b, chunk * kChunk + u / kParts, u / kParts);
-                    multiply(in_f16);
+                    multiply(in_f16, u % kParts);
                 }
             }
         }
@@ -691,13 +772,23 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     if constexpr (kDT == IQ_DTYPE_F16) {
         // Otherwise all is done again with bf16 parts.
         wait_and_meet<0>();
-        if (!__syncthreads_and(exact)) {
+        if (__builtin_expect(!__syncthreads_and(exact), 0)) {
 #pragma unroll
             for (int i = 0; i < kFC; ++i)
 #pragma unroll
                 for (int j = 0; j < kFT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             run(std::false_type());
         }
+    }
+
+    if (kSplit<kDT> > 1 && __builtin_expect(infinite != 0u, 0)) {
+        const raw* rows[kFT];
+#pragma unroll
+        for (int j = 0; j < kFT; ++j) {
+            const int64_t row = min(t.row0 + (wt * kFT + j) * 16 + lane % 16, t.row_end - 1);
+            rows[j] = static_cast<const raw*>(p.x) + (kExperts ? token_of(p, row) : row) * p.ldx;
+        }
+        sum_with_infinities<kDT>(p, t.expert, channel0 + wc * kFC * 16, rows, 0, p.depth, acc);
     }
 
     // Results through LDS, as the matrix instructions leave them (4 channels of a row

@@ -41,7 +41,8 @@ iq_status_t iq_dequantize_groups(const uint8_t* codes, int64_t ldc, const uint8_
 
 /* y[t][n] = sum_k x[t][k] * w[n][k] with w in that format, [channels][depth], depth
  * a multiple of 32.  Products are exact (fp32 activations below 2^-110 lose what they
- * have below 2^-133), sums in fp32, rounded once to the type of y, which is that of x.
+ * have below 2^-133, and those below that count as 0), sums in fp32, rounded once to the
+ * type of y, which is that of x.
  * NaN and infinities pass as in any product of floats; a value of w beyond fp32 (scale
  * bytes from 253 on) counts as infinite.
  * `workspace`: iq_fp4_linear_workspace(...) bytes, 16-byte aligned (NULL where that

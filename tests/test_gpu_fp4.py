@@ -590,3 +590,85 @@ def test_results_do_not_change_from_call_to_call():
         first = iq.fp4_linear(x, w, s)
         for _ in range(5):
             assert torch.equal(iq.fp4_linear(x, w, s), first)
+
+
+# ---------------------------------------------------------------------------
+# Infinite weights
+# ---------------------------------------------------------------------------
+
+INF = float("inf")
+# Ones whose lower bf16 parts are all 0, ones that have them, and what is not finite.
+NEXT_TO_INFINITE = [1.0, 1.00390625, 0.1, 0.0, -1.25, -0.7, 1.5, INF, -INF, float("nan")]
+
+
+def edge_weight(shape, depth, seed):
+    """Small weights [*shape, depth] in whose last group but one value is zero: that has one of
+    16 codes and a scale byte of 250 .. 254, where 253 and 254 reach beyond fp32."""
+    n = int(np.prod(shape))
+    c = torch.randint(0, 16, (n, depth), generator=gen(seed), dtype=torch.uint8)
+    s = torch.randint(118, 124, (n, depth // 32), generator=gen(seed + 1), dtype=torch.uint8)
+    at, i = depth - 27, torch.arange(n)
+    c[:, depth - 32:] = 0
+    c[:, at] = (i % 16).to(torch.uint8)
+    s[:, -1] = (250 + i // 16 % 5).to(torch.uint8)
+    w = (c[:, 0::2] | (c[:, 1::2] << 4)).reshape(*shape, depth // 2)
+    s = s.reshape(*shape, depth // 32)
+    return w.to(DEV), s.to(DEV), ref.values(w.numpy(), s.numpy())
+
+
+def edge_tokens(tokens, depth, seed, dtype):
+    x = torch.randn((tokens, depth), generator=gen(seed)).to(dtype)
+    x[:, depth - 27] = torch.tensor([NEXT_TO_INFINITE[t % 10] for t in range(tokens)]).to(dtype)
+    return x.to(DEV)
+
+
+def edge_product(x, v):
+    """The product and the sum of its terms' magnitudes, the one value of the last group apart:
+    there 0 and infinity meet as they do in floats."""
+    at = x.shape[1] - 27
+    rest, last = x.copy(), x[:, at, None]
+    rest[:, at] = 0.0
+    finite = v.copy()
+    finite[:, at] = 0.0
+    y, size = ref.product(rest, finite)
+    with np.errstate(invalid="ignore"):
+        term = last * v[:, at]
+        return y + term, size + np.abs(term)
+
+
+def check_edges(got, y, size, depth, dtype):
+    """What is beyond the type's largest value, or not finite, has to be so exactly; the rest is
+    within the product's bound.  (No sum is so near to that border that roundings could cross it:
+    the large terms are at most 1.875 2^127 or at least 1.125 2^128, the others below 2^10.)"""
+    got, most = to64(got), torch.finfo(dtype).max
+    with np.errstate(invalid="ignore"):
+        y = np.where(np.abs(y) > most, np.sign(y) * np.inf, y)
+    assert np.array_equal(np.isnan(got), np.isnan(y))
+    inf = np.isinf(y)
+    assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], y[inf])
+    ok = np.isfinite(y)
+    over = np.abs(got[ok] - y[ok]) - ref.product_bound(y[ok], size[ok], depth, dtype)
+    assert (over <= 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("tokens,channels,depth", PRODUCTS)
+def test_infinite_weights(dtype, tokens, channels, depth):
+    x = edge_tokens(tokens, depth, 4, dtype)
+    w, s, v = edge_weight((channels,), depth, 5)
+    y, size = edge_product(to64(x), v)
+    check_edges(iq.fp4_linear(x, w, s), y, size, depth, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("tokens,experts,top_k,channels,depth,dropped,favourite", EXPERT_CASES)
+def test_infinite_weights_by_expert(dtype, tokens, experts, top_k, channels, depth, dropped, favourite):
+    order, _, offsets = routing(tokens, experts, top_k, 11, dropped, favourite)
+    o, f = order.cpu().numpy(), offsets.cpu().numpy()
+    x = edge_tokens(tokens, depth, 4, dtype)
+    w, s, v = edge_weight((experts, channels), depth, 5)
+    y, size = np.zeros((len(o), channels)), np.zeros((len(o), channels))
+    for e in range(experts):
+        rows = slice(int(f[e]), int(f[e + 1]))
+        y[rows], size[rows] = edge_product(to64(x)[o[rows] // top_k], v[e])
+    check_edges(iq.fp4_expert_linear(x, w, s, offsets, order, top_k=top_k), y, size, depth, dtype)
