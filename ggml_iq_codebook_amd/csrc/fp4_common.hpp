@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t codes, uint32_t byte)
 
 // The same as fp16: exact for scale bytes kLowF16 .. kHighF16, where half of the lowest
 // power is 2^-24 and 6 times the highest below 2^16.  Values of other bytes may not be
-// representable.
+// representable, but for 0, which is 0 (NaN for the byte 255) with any of them.
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 constexpr uint32_t kLowF16 = 104, kHighF16 = 140;
 

@@ -110,7 +110,7 @@ __device__ __forceinline__ void split_values(const typename Value<kDT>::raw (&r)
 }
 
 // Whether the values of a lane's groups are exact in fp16: scales within its range, or
-// zeros only.
+// zeros only (NaN where the scale is).
 template <int kN>
 __device__ __forceinline__ bool exact_in_f16(const v4u (&word)[kN], const uint32_t (&byte)[kN])
 {

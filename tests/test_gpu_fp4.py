@@ -672,3 +672,27 @@ def test_infinite_weights_by_expert(dtype, tokens, experts, top_k, channels, dep
         rows = slice(int(f[e]), int(f[e + 1]))
         y[rows], size[rows] = edge_product(to64(x)[o[rows] // top_k], v[e])
     check_edges(iq.fp4_expert_linear(x, w, s, offsets, order, top_k=top_k), y, size, depth, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("tokens", [1, 5, 30, 100, 700])
+def test_a_scale_that_is_nan_counts_over_zeros(dtype, tokens):
+    """A group of zeros whose scale byte is 255 is a group of NaN, and its channel's results are."""
+    channels, depth = 130, 160
+    x = integers((tokens, depth), 1).to(dtype).to(DEV)
+    w, s = random_codes((channels, depth), 2), random_scale((channels, depth // 32), 3, 126, 128)
+    # with any other scale byte it is one of zeros
+    w[20:, 64:] = 0
+    want = iq.fp4_linear(x, w, s)
+    s[20:, 4] = (torch.arange(channels - 20) * 7 % 255).to(torch.uint8).to(DEV)
+    assert torch.equal(iq.fp4_linear(x, w, s), want)
+    w[5, 32:48], s[5, 2] = 0, 255
+    w[77, 64:], s[77, 4] = 0x88, 255                    # -0, a row's last group
+    got = iq.fp4_linear(x, w, s)
+    assert torch.isnan(got[:, [5, 77]]).all()
+    keep = [i for i in range(channels) if i not in (5, 77)]
+    assert torch.equal(got[:, keep], want[:, keep])
+    off = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    by_expert = iq.fp4_expert_linear(x, w[None], s[None], off)
+    assert torch.isnan(by_expert[:, [5, 77]]).all()
+    assert torch.equal(by_expert[:, keep], want[:, keep])
