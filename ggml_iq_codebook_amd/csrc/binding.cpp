@@ -759,7 +759,7 @@ PyMethodDef methods[] = {
     method<int8_linear, 5, true>("int8_linear"),
     method<int8_expert_matmul, 9, true>("int8_expert_matmul"),
     method<quantize_groups, 2, false>("quantize_groups"),
-    method<dequantize_groups, 4, false>("dequantize_groups"),
+    method<dequantize_groups, 4, true>("dequantize_groups"),
     method<fp4_linear, 4, true>("fp4_linear"),
     method<fp4_expert_linear, 7, true>("fp4_expert_linear"),
     method<expert_gate, 4, true>("expert_gate"),

@@ -277,7 +277,10 @@ def quantize_groups(w, *, status=None, check=True):
 def dequantize_groups(codes, scale, *, dtype=torch.float32, out=None):
     """What ``quantize_groups`` wrote, as values in ``dtype`` (or in the type of ``out``):
     [rows, cols].  They are exact in fp32 and bf16, rounded in fp16."""
-    return (_binding or _native()).dequantize_groups(codes, scale, dtype, out)
+    result = (_binding or _native()).dequantize_groups(codes, scale, dtype, out)
+    if result is NotImplemented:
+        _no_out(out)                  # codes and scales have no gradient
+    return result
 
 
 def fp4_linear(x, w, w_scale, *, out=None):
