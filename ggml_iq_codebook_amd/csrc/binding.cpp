@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -704,12 +705,19 @@ PyObject* expert_combine_backward(PyObject* const* a)
 
 PyObject* iq_error = nullptr;         // the package's exception class
 
-// Whether autograd records what is done with these arguments.
+// Whether autograd records what is done with these arguments, or carries a tangent of one
+// of them along (forward mode, which torch.no_grad() does not turn off).  The functions of the
+// graph have no rule for tangents, and raise.
 bool recorded(PyObject* const* args, Py_ssize_t count)
 {
-    if (!at::GradMode::is_enabled()) return false;
-    for (Py_ssize_t i = 0; i < count; ++i)
-        if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad()) return true;
+    const bool graph = at::GradMode::is_enabled();
+    const bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    if (!graph && !tangents) return false;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        if (!THPVariable_Check(args[i])) continue;
+        const at::Tensor& t = THPVariable_Unpack(args[i]);
+        if ((graph && t.requires_grad()) || (tangents && t._fw_grad(/*level=*/0).defined())) return true;
+    }
     return false;
 }
 

@@ -20,7 +20,8 @@ Autograd: ``expert_gate``, ``expert_balance``, ``expert_dispatch``, its gradient
 the other gradients have no gradient: a backward pass that reaches their results
 raises.  ``quantize_rows``, ``quantize_groups`` and ``expert_sort`` answer with
 integers and scales of them, which are constants.  ``out`` cannot be given where
-gradients are recorded.
+gradients are recorded.  No operator has a rule for forward mode: a tensor with a
+tangent is refused.
 """
 
 from __future__ import annotations
@@ -101,6 +102,7 @@ def _word(status, check, like):
 
 # --- autograd: what the calls below turn to when the binding answers
 # NotImplemented, because gradients are being recorded for one of the arguments
+# (or one has a tangent, which makes a Function raise)
 
 def _rows(grad):
     """A gradient as the kernels take it: consecutive values in a row."""

@@ -4,6 +4,7 @@ import sys
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,59 @@ def test_values_are_not_written_into_a_recorded_tensor():
     with torch.no_grad():
         assert iq.dequantize_groups(codes, scale, out=leaf) is leaf
     assert torch.equal(leaf.detach(), want)
+
+
+def calls():
+    """Every call that autograd could record, by one of its floating-point arguments."""
+    x, logits = normal((6, 64), 1), normal((6, 8), 2)
+    w, s = iq.quantize_groups(normal((10, 64), 3))
+    q, qs = iq.quantize_rows(normal((10, 64), 3))
+    xq, xs = iq.quantize_rows(x)
+    choice, weights = iq.expert_gate(logits, 2)
+    order, position, offsets = iq.expert_sort(choice, 8)
+    _, counts, live = iq.expert_balance(logits, choice)
+    rows, grad, loss_grad = normal((12, 64), 4), normal((6, 2), 5), torch.ones((), device=DEV)
+    one = torch.tensor([0, 6], dtype=torch.int32, device=DEV)
+    return [
+        ("expert_gate", lambda v: iq.expert_gate(v, 2), logits),
+        ("expert_gate of probabilities", lambda v: iq.expert_gate(v, 2, renormalize=False), logits),
+        ("expert_gate_backward", lambda v: iq.expert_gate_backward(v, logits, choice, weights), grad),
+        ("expert_gate_backward, logits",
+         lambda v: iq.expert_gate_backward(grad, v, choice, weights, renormalize=False), logits),
+        ("expert_gate_backward, weights", lambda v: iq.expert_gate_backward(grad, logits, choice, v), weights),
+        ("expert_balance", lambda v: iq.expert_balance(v, choice), logits),
+        ("expert_balance_backward", lambda v: iq.expert_balance_backward(v, logits, counts, live), loss_grad),
+        ("expert_balance_backward, logits",
+         lambda v: iq.expert_balance_backward(loss_grad, v, counts, live), logits),
+        ("fp4_linear", lambda v: iq.fp4_linear(v, w, s), x),
+        ("fp4_linear, out", lambda v: iq.fp4_linear(x, w, s, out=v), normal((6, 10), 6)),
+        ("fp4_expert_linear", lambda v: iq.fp4_expert_linear(v, w[None], s[None], one), x),
+        ("dequantize_groups, out", lambda v: iq.dequantize_groups(w, s, out=v), normal((10, 64), 7)),
+        ("int8_linear", lambda v: iq.int8_linear(v, q, qs), x),
+        ("int8_matmul", lambda v: iq.int8_matmul(xq, v, q, qs), xs),
+        ("int8_expert_matmul", lambda v: iq.int8_expert_matmul(xq, v, q[None], qs[None], one), xs),
+        ("expert_dispatch", lambda v: iq.expert_dispatch(v, position, offsets), x),
+        ("expert_dispatch_backward", lambda v: iq.expert_dispatch_backward(v, position, offsets), rows),
+        ("expert_combine", lambda v: iq.expert_combine(v, position, offsets, weights), rows),
+        ("expert_combine, weights", lambda v: iq.expert_combine(rows, position, offsets, v), weights),
+        ("expert_combine_backward",
+         lambda v: iq.expert_combine_backward(x, v, position, offsets, weights), rows),
+    ]
+
+
+@pytest.mark.parametrize("recording", [True, False])
+def test_tangents_are_refused(recording):
+    """No operator has a rule for forward mode; an answer without the tangent would count as
+    a constant.  (Forward mode goes on under no_grad, in torch's functions too.)"""
+    for name, call, value in calls():
+        value = value.clone()
+        before = value.clone()
+        with torch.set_grad_enabled(recording), fwd.dual_level():
+            dual = fwd.make_dual(value, torch.ones_like(value))
+            with pytest.raises((NotImplementedError, ValueError)):
+                call(dual)
+                pytest.fail("%s answered without a tangent" % name)
+            assert torch.equal(value, before), name
+            # its value alone is an ordinary tensor
+            call(fwd.unpack_dual(dual).primal.detach())
+        call(value)
