@@ -144,18 +144,23 @@ class _Combine(Function):
 
 
 class _Gate(Function):
+    # The gradient of renormalized weights does not read the logits: they are not kept.
     @staticmethod
     def forward(ctx, logits, top_k, renormalize, status):
         choice, weights = _binding.expert_gate(logits, top_k, renormalize, status)
         ctx.mark_non_differentiable(choice)
-        ctx.save_for_backward(logits, choice, weights)
-        ctx.renormalize = renormalize
+        ctx.save_for_backward(choice, weights, *(() if renormalize else (logits,)))
+        ctx.like = logits.shape[1], logits.dtype
         return choice, weights
 
     @staticmethod
     def backward(ctx, _, grad):
-        return expert_gate_backward(grad.contiguous(), *ctx.saved_tensors,
-                                    renormalize=ctx.renormalize), None, None, None
+        choice, weights, *kept = ctx.saved_tensors
+        experts, dtype = ctx.like
+        # (the type and shape alone: one row for all tokens)
+        logits = kept[0] if kept else weights.new_empty((1, experts), dtype=dtype).expand(len(weights), experts)
+        return expert_gate_backward(grad.contiguous(), logits, choice, weights,
+                                    renormalize=not kept), None, None, None
 
 
 class _Balance(Function):

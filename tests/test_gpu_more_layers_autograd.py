@@ -99,3 +99,30 @@ def test_tangents_are_refused(recording):
             # its value alone is an ordinary tensor
             call(fwd.unpack_dual(dual).primal.detach())
         call(value)
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_logits_written_over_after_the_gate(renormalize):
+    """The gradient of renormalized weights does not read the logits: they may be written over
+    (masked for the next pass, say) and need not be kept.  That of probabilities does."""
+    for dtype in (torch.float32, torch.bfloat16):
+        leaf = normal((9, 8), 1, dtype).requires_grad_()
+        grad = normal((9, 3), 2)
+        _, weights = iq.expert_gate(leaf * 1.0, 3, renormalize=renormalize)
+        want, = torch.autograd.grad(weights, leaf, grad)
+        logits = leaf * 1.0
+        _, weights = iq.expert_gate(logits, 3, renormalize=renormalize)
+        logits.masked_fill_(torch.ones((9, 8), dtype=torch.bool, device=DEV), -float("inf"))
+        if renormalize:
+            got, = torch.autograd.grad(weights, leaf, grad, allow_unused=True)
+            assert got is not None and got.dtype == dtype
+            # masked_fill_ comes behind the gate in the graph and takes nothing from its gradient
+            assert torch.equal(got, want)
+        else:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                torch.autograd.grad(weights, leaf, grad)
+    # without tokens
+    empty = torch.empty((0, 8), device=DEV, requires_grad=True)
+    _, weights = iq.expert_gate(empty, 3, renormalize=renormalize)
+    weights.sum().backward()
+    assert empty.grad.shape == (0, 8)
