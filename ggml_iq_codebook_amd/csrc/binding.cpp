@@ -517,7 +517,8 @@ PyObject* expert_gate(PyObject* const* a)
     const int32_t top_k = int32_of(a[1], "top_k");
     const bool renormalize = bool_of(a[2], "renormalize");
     int32_t* status = status_word(c, a[3]);
-    const int64_t k = std::max(top_k, 0);
+    // The library refuses others, for which no room is made.
+    const int64_t k = top_k > 0 && top_k <= l.cols ? top_k : 0;
     at::Tensor choice = at::empty({l.rows, k}, c.options(at::kInt));
     at::Tensor weights = at::empty({l.rows, k}, c.options(at::kFloat));
     check(unlocked([&] {

@@ -454,3 +454,15 @@ def test_a_training_step_of_the_router():
     assert ((l.grad.double().cpu() - torch.nan_to_num(l64.grad)).abs() <= 128 * 2.0 ** -24 * size).all()
     assert (x.grad.double().cpu() - x64.grad).abs().max() <= 64 * 2.0 ** -24 * 50
     assert l.grad.any() and x.grad.any()
+
+
+def test_more_choices_than_experts_are_refused_before_room_is_made_for_them():
+    l = normal((6, 10), 1)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for top_k in (11, 10 ** 6):
+        with pytest.raises(iq.IQError) as e:
+            iq.expert_gate(l, top_k)
+        assert e.value.name == "IQ_ERR_SHAPE"
+    assert torch.cuda.max_memory_allocated() - before < 10 ** 6
