@@ -204,6 +204,16 @@ __device__ __forceinline__ void sum_with_infinities(const Fp4Product& p, int exp
     }
 }
 
+// What the wave's lanes have written to LDS is there for its other lanes, and what they have
+// read may be written over.  A wave's LDS accesses are done in order, so this is for the
+// compiler, which must not move one across.
+__device__ __forceinline__ void order_in_wave()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 4 consecutive channels of one row of y, in its type.
 template <int kDT>
 __device__ __forceinline__ void store_channels(const Fp4Product& p, int64_t row, int channel, v4f f)
@@ -391,7 +401,9 @@ __global__ __launch_bounds__(kWaves* kWave) void fp4_few_kernel(Fp4Product p, in
                 const int s = s1 + j;
                 if (s >= last) break;
                 if (j % kSub == 0) {
+                    order_in_wave();
                     stage_x();
+                    order_in_wave();
                     if (s + kSub < last) fetch_x(s + kSub);
                 }
                 multiply(j % kSub, codes[h][j], scales[h], j);
@@ -812,8 +824,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
                                                       4 * sizeof(raw)),
                              o, sizeof(o));
         }
-        // A wave's own LDS accesses are done in order.
-        __builtin_amdgcn_wave_barrier();
+        order_in_wave();
 #pragma unroll
         for (int s = 0; s < (16 * kLanes + kWave - 1) / kWave; ++s) {
             const int r = (s * kWave + lane) / kLanes, c = (s * kWave + lane) % kLanes * kN;
@@ -830,7 +841,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
                     if (channel + v < p.channels) to[v] = o[v];
             }
         }
-        __builtin_amdgcn_wave_barrier();
+        order_in_wave();
     }
 }
 
