@@ -494,10 +494,9 @@ struct Parts {
 // kWT x kWC waves share a tile of kRows rows of y by kChannels channels, each a
 // part of kRows/kWT by kChannels/kWC, in steps of 128 of the depth.  The activations
 // go through a ring of kStages buffers in LDS that direct copies fill kStages - 1
-// steps ahead.  The weight comes in chunks of kChunk steps, through registers into
-// two buffers of codes (any alignment, whole cache lines of its rows), its scales 8
-// steps at a time, and becomes bf16 where it is multiplied, four instructions for 8
-// values.
+// steps ahead.  The weight comes step by step through registers into two buffers of
+// codes (any alignment), its scales 8 steps at a time, and becomes bf16 where it is
+// multiplied, four instructions for 8 values.
 //
 // Of eight waves, two on a SIMD, the second half runs half a step behind (ping-pong): on
 // each SIMD one wave multiplies while the other reads its operands.  A step is two
@@ -510,8 +509,7 @@ struct Parts {
 // LDS in steps of 64 of the depth 147, of 128 128, copies by a buffer's 32-bit offsets
 // 124.  Smaller tiles fill the card where there are few: 1021 x 2049 x 1568 in
 // bf16 64 x 64 with four waves 17.4 us, with two halves in turn 24.
-template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
-          bool kExperts>
+template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel(Fp4Product p,
                                                                                Parts parts,
                                                                                int channel_tiles)
@@ -523,8 +521,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     constexpr int kParts = kStaged<kDT>;
     constexpr int kRowsPerLoad = 4;   // of 256 bytes each
     constexpr int kLoads = kRows / kRowsPerLoad / kWaves;
-    // Groups of a chunk, 16 bytes of codes each, and a thread's part of them.
-    constexpr int kGroups = 4 * kChunk, kCodes = kChannels * kGroups / kThreads;
+    // Groups of a step, 16 bytes of codes each, and a thread's part of them.
+    constexpr int kGroups = kPiece / kGroup, kCodes = kChannels * kGroups / kThreads;
     // Scales come for more steps at once, 16 groups to a thread: what they cost is the
     // cache lines they are spread over.
     constexpr int kScales = 32, kScaleThreads = kChannels * kScales / 16;
@@ -590,15 +588,15 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     const int channel0 = t.channel_tile * kChannels;
     const uint8_t* w = p.w + t.expert * p.w_stride + (int64_t)channel0 * p.ldw;
     const uint8_t* scale = p.scale + t.expert * p.s_stride + (int64_t)channel0 * p.lds;
-    // Row r's group g of a chunk in slot g ^ slot(r).
-    auto slot = [](int r) { return kGroups == 8 ? r % 8 : r / 2 % kGroups; };
+    // Row r's group g of a step in slot g ^ slot(r).
+    auto slot = [](int r) { return r / 2 % kGroups; };
     v4u codes[kCodes];
-    auto fetch_codes = [&](int chunk) {
+    auto fetch_codes = [&](int piece) {
 #pragma unroll
         for (int i = 0; i < kCodes; ++i) {
             const int q = i * kThreads + threadIdx.x, r = q / kGroups;
             const int n = min(r, p.channels - 1 - channel0);
-            const int g = min(chunk * kGroups + ((q % kGroups) ^ slot(r)), groups - 1);
+            const int g = min(piece * kGroups + ((q % kGroups) ^ slot(r)), groups - 1);
             codes[i] = load16(w + ((uint32_t)n * (uint32_t)p.ldw + g * (kGroup / 2)));
         }
     };
@@ -608,11 +606,11 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     };
     // Groups beyond the last, whose activations are zeros, have the scale 1.
     v4u scales = {};
-    auto fetch_scales = [&](int chunk) {
+    auto fetch_scales = [&](int turn) {
         if (threadIdx.x >= kScaleThreads) return;
         const int n = min((int)threadIdx.x / 2, p.channels - 1 - channel0);
         const uint8_t* s = scale + (uint32_t)n * (uint32_t)p.lds;
-        const int g0 = chunk * kScales + threadIdx.x % 2 * 16;
+        const int g0 = turn * kScales + threadIdx.x % 2 * 16;
         if (g0 + 16 <= groups)
             scales = load16(s + g0);
         else
@@ -629,12 +627,12 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     v8bf x[4][kFT];
     v4u word[kFC];
     uint32_t byte[kFC];
-    // The ring's buffer b, and step `piece` of the weight, the one `in_chunk` of its chunk.
-    auto read = [&](int b, int piece, int in_chunk) {
+    // The ring's buffer b, and the weight of step `piece` of the depth.
+    auto read = [&](int b, int piece) {
 #pragma unroll
         for (int i = 0; i < kFC; ++i) {
-            const int r = (wc * kFC + i) * 16 + lane % 16, g = 4 * in_chunk + quarter;
-            word[i] = staged.codes[piece / kChunk % 2][r * kGroups + (g ^ slot(r))];
+            const int r = (wc * kFC + i) * 16 + lane % 16;
+            word[i] = staged.codes[piece % 2][r * kGroups + (quarter ^ slot(r))];
             byte[i] = reinterpret_cast<const uint8_t*>(
                 &staged.scales[4 * piece / kScales % 2][r * kScaleRow])[4 * piece % kScales + quarter];
         }
@@ -698,7 +696,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
         }
     };
 
-    const int steps = (groups + 3) / 4 * kParts;
+    const int pieces = (groups + 3) / 4;
     auto run = [&](auto in_f16) {
         fetch_codes(0);
         fetch_scales(0);
@@ -711,47 +709,45 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
         fetch_scales(1);
         fetch_codes(1);
         constexpr int kLeft = (kStages - 2) * kLoads;
-        // A chunk of the weight is as many steps of each part of the activations.
-        constexpr int kSteps = kChunk * kParts, kTurn = kScales / kGroups;
+        constexpr int kTurn = kScales / kGroups;
         int buffer = 0;
-        auto store_weight = [&](int chunk) {
-            store_codes((chunk + 1) % 2);
-            if (chunk % kTurn == 0) store_scales((chunk / kTurn + 1) % 2);
+        auto store_weight = [&](int piece) {
+            store_codes((piece + 1) % 2);
+            if (piece % kTurn == 0) store_scales((piece / kTurn + 1) % 2);
         };
-        // Step s + kStages - 1 into the buffer of the step before s, and at a chunk's first
-        // step (u) the weight two chunks ahead.
-        auto fetch_ahead = [&](int s, int u, int chunk) {
-            fetch(buffer == 0 ? kStages - 1 : buffer - 1, s + kStages - 1);
+        // A step of the depth is one of each part of the activations.  The one kStages - 1
+        // ahead goes into the buffer of the one before, and with the first part the weight two
+        // steps ahead is asked for.
+        auto fetch_ahead = [&](int piece, int part) {
+            fetch(buffer == 0 ? kStages - 1 : buffer - 1, piece * kParts + part + kStages - 1);
             buffer = buffer + 1 == kStages ? 0 : buffer + 1;
-            if (u == 0) {
+            if (part == 0) {
                 __builtin_amdgcn_sched_barrier(0);
-                if (chunk % kTurn == 0) fetch_scales(chunk / kTurn + 2);
-                fetch_codes(chunk + 2);
+                if (piece % kTurn == 0) fetch_scales(piece / kTurn + 2);
+                fetch_codes(piece + 2);
             }
         };
         if constexpr (kPingPong) {
             const bool late = wave >= kWaves / 2;
             wait_and_meet<kLeft + kCodes>();
             if (late) asm volatile("s_barrier" ::: "memory");
-            for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+            for (int piece = 0; piece < pieces; ++piece) {
 #pragma unroll
-                for (int u = 0; u < kSteps; ++u) {
-                    const int s = s0 + u;
-                    if (s >= steps) break;
-                    // The chunk before, whose buffer this is, was read before the last barrier,
-                    // as both halves read the step before.
-                    if (u == 0) store_weight(chunk);
-                    read(buffer, chunk * kChunk + u / kParts, u / kParts);
-                    fetch_ahead(s, u, chunk);
+                for (int part = 0; part < kParts; ++part) {
+                    // The weight's step before, whose buffer this is, was read before the last
+                    // barrier, as both halves read the step before.
+                    if (part == 0) store_weight(piece);
+                    read(buffer, piece);
+                    fetch_ahead(piece, part);
                     // The next step has to be there.  The weight's codes were asked for behind
-                    // the copies of step s0 + kStages - 1.
-                    if (u <= kStages - 2)
+                    // the copies of the step kStages - 1 behind its first part's.
+                    if (part <= kStages - 2)
                         wait_and_meet<kLeft + kCodes>();
                     else
                         wait_and_meet<kLeft>();
                     __builtin_amdgcn_sched_barrier(0);
                     __builtin_amdgcn_s_setprio(1);
-                    multiply(in_f16, u % kParts);
+                    multiply(in_f16, part);
                     __builtin_amdgcn_s_setprio(0);
                     __builtin_amdgcn_sched_barrier(0);
                     asm volatile("s_barrier" ::: "memory");
@@ -759,23 +755,21 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
             }
             if (!late) asm volatile("s_barrier" ::: "memory");
         } else {
-            for (int s0 = 0, chunk = 0; s0 < steps; s0 += kSteps, ++chunk) {
+            for (int piece = 0; piece < pieces; ++piece) {
 #pragma unroll
-                for (int u = 0; u < kSteps; ++u) {
-                    const int s = s0 + u;
-                    if (s >= steps) break;
+                for (int part = 0; part < kParts; ++part) {
                     // This step has to be there, and the others are done with the one before.
-                    // The codes last asked for are behind the copies of the chunk's step
-                    // kStages - 1, or of that step of the chunk before.
-                    if (u == 0 ? kSteps < kStages : u < kStages)
+                    // The codes last asked for are behind the copies of the step kStages - 1
+                    // behind this weight's first part's, or the weight's before.
+                    if (part == 0 ? kParts < kStages : part < kStages)
                         wait_and_meet<kLeft + kCodes>();
                     else
                         wait_and_meet<kLeft>();
-                    if (u == 0) store_weight(chunk);
+                    if (part == 0) store_weight(piece);
                     const int b = buffer;
-                    fetch_ahead(s, u, chunk);
-                    read(b, chunk * kChunk + u / kParts, u / kParts);
-                    multiply(in_f16, u % kParts);
+                    fetch_ahead(piece, part);
+                    read(b, piece);
+                    multiply(in_f16, part);
                 }
             }
         }
@@ -890,8 +884,7 @@ bool direct(int dtype, const void* x, int64_t ldx, int64_t tokens)
            (ldx % 8 == 0 || tokens == 1) && ldx <= kNear;
 }
 
-template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, int kChunk,
-          bool kExperts>
+template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, bool kExperts>
 hipError_t launch_tiles(const Fp4Product& p, const Parts& parts, hipStream_t stream)
 {
     const int channel_tiles = (p.channels + kChannels - 1) / kChannels;
@@ -899,8 +892,7 @@ hipError_t launch_tiles(const Fp4Product& p, const Parts& parts, hipStream_t str
     return in_parts(workgroups(p, kRows, channel_tiles), kWT * kWC * kWave,
                     [&](int64_t first, dim3 wgs) {
         part.first_tile = first;
-        hipLaunchKernelGGL((fp4_tile_kernel<kDT, kRows, kChannels, kWT, kWC, kStages, kChunk,
-                                            kExperts>),
+        hipLaunchKernelGGL((fp4_tile_kernel<kDT, kRows, kChannels, kWT, kWC, kStages, kExperts>),
                            wgs, dim3(kWT * kWC * kWave), 0, stream, part, parts, channel_tiles);
         return hipGetLastError();
     });
@@ -950,10 +942,10 @@ hipError_t launch_dense(int size, const Fp4Product& p, const Parts& x, hipStream
         // The parts of 32 rows of fp32 do not fit LDS.
         if constexpr (kDT != IQ_DTYPE_F32) return launch_few<kDT, 32, 2, 8, false>(p, stream);
         break;
-    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, 1, false>(p, x, stream);
-    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, 1, false>(p, x, stream);
-    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, 1, false>(p, x, stream);
-    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, false>(p, x, stream);
+    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, false>(p, x, stream);
+    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, false>(p, x, stream);
+    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, false>(p, x, stream);
+    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, false>(p, x, stream);
     default: break;
     }
     return launch_few<kDT, 16, 1, 4, false>(p, stream);
@@ -970,10 +962,10 @@ hipError_t launch_experts(int size, const Fp4Product& p, const Parts& x, hipStre
         // fp16 has a faster one always.
         if constexpr (kDT != IQ_DTYPE_F16) return launch_few<kDT, 8, 2, 4, true>(p, stream);
         break;
-    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, 1, true>(p, x, stream);
-    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, 1, true>(p, x, stream);
-    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, 1, true>(p, x, stream);
-    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, 1, true>(p, x, stream);
+    case size_key(32, 64, 4): return launch_tiles<kDT, 32, 64, 1, 4, 2, true>(p, x, stream);
+    case size_key(32, 128, 4): return launch_tiles<kDT, 32, 128, 1, 4, 2, true>(p, x, stream);
+    case size_key(64, 128, 4): return launch_tiles<kDT, 64, 128, 1, 4, 2, true>(p, x, stream);
+    case size_key(128, 256, 8): return launch_tiles<kDT, 128, 256, 2, 4, 3, true>(p, x, stream);
     default: break;
     }
     return launch_few<kDT, 16, 2, 4, true>(p, stream);
