@@ -16,7 +16,8 @@
 // over the logits (16384 x 64: 5.8 us; 65536 x 256: 23 us, 5.8 TB/s with what the
 // last level of caches holds).  The loss's forward pass keeps a column's sum in the lanes
 // that have it and asks for the next row while it works on one (65536 x 256: 20.4 us,
-// 3.3 TB/s, bound by its exponentials and sums).
+// 3.3 TB/s, bound by its exponentials and sums, and by LDS, where the counts by atomics
+// and the waves' columns meet on banks in 40 % of its active cycles).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -302,7 +303,9 @@ __device__ __forceinline__ void finish(const double* probability, const int* cou
 
 // A workgroup's part of the tokens: sums of the probabilities (fp32 over up to 32
 // rows a lane, fp64 beyond), counts of the choices and live tokens.  Alone it
-// finishes; otherwise its sums go to the workspace.
+// finishes; otherwise its sums go to the workspace, rounded to fp32 (2^-24 of a sum of
+// positive terms, no more than the probabilities themselves are off, for half of the
+// bytes that the finishing workgroups wait for) and added up in fp64 there.
 template <int kDT, int kL, int kC, bool kAlone>
 __global__ __launch_bounds__(kSumThreads) void expert_balance_kernel(
     Logits l, const void* __restrict__ choice, int choice_bytes, int top_k, float* loss,

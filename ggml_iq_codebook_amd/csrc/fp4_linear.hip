@@ -503,12 +503,12 @@ struct Parts {
 // barriers long.  Four waves go together, a step a barrier, and it is other workgroups
 // of the compute unit that fill the gaps.
 //
-// 128 x 256 at 4096^3 in bf16: 117 us, 1170 TFLOP/s, the matrix cores 52 % busy; a library
-// product of the unpacked weight 97 to 104.  On the way there: the weight straight to
-// registers each step 260 us (a load that touches 16 rows takes 75 cycles to issue), through
-// LDS in steps of 64 of the depth 147, of 128 128, copies by a buffer's 32-bit offsets
-// 124.  Smaller tiles fill the card where there are few: 1021 x 2049 x 1568 in
-// bf16 64 x 64 with four waves 17.4 us, with two halves in turn 24.
+// 128 x 256 at 4096^3 in bf16: 114 us waited for singly, 1210 TFLOP/s, the matrix cores 54 %
+// busy, and what they wait for LDS reads and conversions; a library product of the unpacked
+// weight 97 to 104.  On the way there: the weight straight to registers each step 260 us (a
+// load that touches 16 rows takes 75 cycles to issue), through LDS in steps of 64 of the depth
+// 147, of 128 128, copies by a buffer's 32-bit offsets 124.  Smaller tiles fill the card where
+// there are few: 1021 x 2049 x 1568 in bf16 takes 18.7 us with 32 x 64.
 template <int kDT, int kRows, int kChannels, int kWT, int kWC, int kStages, bool kExperts>
 __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel(Fp4Product p,
                                                                                Parts parts,
@@ -551,7 +551,7 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     // (4 k + q) ^ (row % 16).  A read of 16 bytes a lane takes 16 lanes at a time, four
     // neighbours each of different rows and quarters of the wave: with q in the low bits
     // they meet different banks (with 4 q + k two and two meet, 39 % more LDS cycles:
-    // 4096^3 120 us, now 117).  Rows beyond the last repeat it: their results are not stored.
+    // 4096^3 120 us against 117).  Rows beyond the last repeat it: their results are not stored.
     auto column = [&](int i) {
         const int c = (lane % 16) ^ ((wave * kLoads + i) * kRowsPerLoad + lane / 16) % 16;
         return (c % 4 * 4 + c / 4) * 8;
@@ -776,7 +776,8 @@ __global__ __launch_bounds__(kWT* kWC* kWave, kWT* kWC / 4) void fp4_tile_kernel
     };
     run(std::bool_constant<kDT == IQ_DTYPE_F16>());
     if constexpr (kDT == IQ_DTYPE_F16) {
-        // Otherwise all is done again with bf16 parts.
+        // Otherwise all is done again with bf16 parts: 2048 x 4096 x 4096 61 us, with scales
+        // out of range everywhere 244.
         wait_and_meet<0>();
         if (__builtin_expect(!__syncthreads_and(exact), 0)) {
 #pragma unroll

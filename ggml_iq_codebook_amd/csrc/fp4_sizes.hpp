@@ -3,13 +3,18 @@
 //
 // Sizes of 64 channels and more are the tile kernel's, the others those of the kernel
 // of few rows, which reads a weight again for each of its row tiles and is taken up to
-// 12 of them.  Dense products of few rows have a workgroup to a compute unit, whose
+// 12 of them.  (That limit was set by hand, these sizes were hardly timed beyond it, and just
+// beyond it is the worst choice of all: fp32 193 x 1092 x 4800 takes 32 x 64 and 56 us, where
+// 16 x 32 took 28.)  Dense products of few rows have a workgroup to a compute unit, whose
 // eight waves share the depth; those by expert have many, and smaller ones hide each
-// other's start (16 tokens, 2 of 16 experts of 1536 x 4096: 20.7 us with eight waves of
-// 4 x 16, 15.1 with four of 4 x 32).  The constants are fits to measured times, made by
-// perf/fp4_sizes.py from profiles/sizes_fp4.json.  The times hold for 256 compute units,
-// a whole card: the choice also sizes the workspace, which has to be the same wherever
-// it is asked.
+// other's start (16 tokens, 2 of 16 experts of 1536 x 4096, at the time this was decided:
+// 20.7 us with eight waves of 4 x 16, 15.1 with four of 4 x 32; 8 x 32 took the latter's
+// place).  The constants are fits to measured times, made by perf/fp4_sizes.py from
+// profiles/sizes_fp4.json.  The times are those of earlier kernels than these: fp32 and
+// bf16 from before fp16 activations were multiplied as fp16, fp16 from after that, all from
+// before the tile kernel's slots without bank conflicts and its loop in fewer registers,
+// which made tiles up to 10 % faster.  They hold for 256 compute units, a whole card: the
+// choice also sizes the workspace, which has to be the same wherever it is asked.
 #pragma once
 
 #include <cmath>

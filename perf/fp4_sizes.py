@@ -2,10 +2,12 @@
 waves a workgroup of a product with 4-bit weights has.
 
 ``profiles/sizes_fp4.json`` holds the microseconds of every size, "rows x channels
-waves" (null: not timed, far from the fastest) in products [rows, channels, depth,
-experts], by type of the activations, dense and by expert.  They are GPU times in
-captured graphs on MI355X, 256 compute units, three weights in turn, the launch that
-splits fp16 and fp32 activations included where the size needs it.
+waves" (null: not timed, far from the fastest or beyond the limit in ``taken``) in
+products [rows, channels, depth, experts], by type of the activations, dense and by
+expert.  They are GPU times in captured graphs on MI355X, 256 compute units, three
+weights in turn, the launch that splits fp32 activations included where the size needs
+it.  The kernels have changed since (the sizes' header says how), and no program here
+takes the times: the library has no way to ask for a size.
 
     python perf/fp4_sizes.py
 
@@ -72,7 +74,8 @@ def fit(data):
 
 
 def taken(size, rows, experts):
-    """Sizes of few rows read a weight again for each of their row tiles: up to 12."""
+    """Sizes of few rows read a weight again for each of their row tiles: up to 12, a limit
+    set by hand, beyond which they were hardly timed."""
     tall, wide, _ = numbers(size)
     return wide >= 64 or rows / max(experts, 1) <= 12 * tall
 
